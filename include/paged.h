@@ -58,7 +58,10 @@ typedef enum {
 typedef enum {
   PA_F16 = 0,      /* IEEE binary16 */
   PA_BF16 = 1,     /* bfloat16 */
-  PA_FP8_E4M3 = 2  /* OCP FP8 E4M3 (bias 7, max finite 448, no infinities) */
+  PA_FP8_E4M3 = 2, /* OCP FP8 E4M3 (bias 7, max finite 448, no infinities) */
+  PA_MXFP4 = 3     /* OCP MX v1.0 MXFP4: E2M1 codes with an E8M0 scale per 32 elements; the
+                      type of the caches of the pa_*_mxfp4 calls, given to the workspace
+                      sizing calls */
 } pa_dtype;
 
 /* Thread-local description of the last failing call on this thread ("" if none). */
@@ -348,6 +351,158 @@ PA_API pa_status pa_copy_blocks(const void* src_key_cache, const void* src_value
                                 int32_t* error_word, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* A cache held in 4 bits (MXFP4).                                            */
+/* ------------------------------------------------------------------------- */
+/*
+ * [P4] stores K/V in FP8 to halve the cache; this is the next halving, in the
+ * format of the OCP Microscaling specification v1.0 (MXFP4). 32 consecutive
+ * elements of a row share one scale byte b and element i is
+ *     E2M1(code_i) * 2^(b - 127),   b = 255: NaN (the whole block of 32);
+ * a byte of 0 reads as 0. E2M1 is sign and magnitude {0, .5, 1, 1.5, 2, 3, 4, 6}.
+ * A cache is four planes, one kv-head's rows of a block lying together:
+ *   key_cache, value_cache  uint8 [num_blocks, num_kv_heads, block_size, head_dim / 2],
+ *                           element 2i of a row in the low half of byte i
+ *   k_scales, v_scales      uint8 [num_blocks, num_kv_heads, block_size, head_dim / 32]
+ * Every plane is 16-byte aligned. A block of a plane is contiguous, so
+ * pa_copy_blocks, pa_fork_sequences and pa_compact_blocks take them as they are.
+ * head_dim in {64, 128}; block_size in {16, 32}.
+ */
+
+/*
+ * pa_reshape_and_cache into an MXFP4 cache: per 32 elements x of a row
+ *     b = clamp(floor(log2 max|x|) - 2, -126, 125) + 127,
+ *     code_i = E2M1(x_i * 2^(127 - b)), nearest even, saturating at 6;
+ * a block with an infinity or a NaN gets b = 255. key, value: [num_tokens,
+ * num_kv_heads, head_dim] of kv_dtype (F16 or BF16). slot_mapping as in
+ * pa_reshape_and_cache: a token whose slot is negative or outside the pool is
+ * not written.
+ */
+PA_API pa_status pa_reshape_and_cache_mxfp4(const void* key, const void* value, uint8_t* key_cache,
+                                            uint8_t* value_cache, uint8_t* k_scales,
+                                            uint8_t* v_scales, const int32_t* slot_mapping,
+                                            int32_t num_tokens, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size,
+                                            int64_t num_blocks, pa_dtype kv_dtype,
+                                            pa_stream_t stream);
+
+/*
+ * The reverse: rows of an MXFP4 cache by slot, as 16-bit values (rounded to
+ * kv_dtype: exact within its range). key, value [num_tokens, num_kv_heads,
+ * head_dim] of kv_dtype are written; the rows of a token whose slot is negative
+ * or outside the pool are left as they were. A slot may be read several times.
+ */
+PA_API pa_status pa_gather_cache_mxfp4(void* key, void* value, const uint8_t* key_cache,
+                                       const uint8_t* value_cache, const uint8_t* k_scales,
+                                       const uint8_t* v_scales, const int32_t* slot_mapping,
+                                       int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int64_t num_blocks, pa_dtype kv_dtype,
+                                       pa_stream_t stream);
+
+/*
+ * pa_decode over an MXFP4 cache: the same operation, arguments, limits,
+ * workspace (pa_decode_workspace_size with PA_MXFP4) and run-time table
+ * errors; q_dtype F16 or BF16. A NaN block of K makes the output rows of its
+ * kv-head NaN, one of V the 32 outputs it belongs to.
+ */
+PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* key_cache,
+                                 const uint8_t* value_cache, const uint8_t* k_scales,
+                                 const uint8_t* v_scales, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 int64_t num_blocks, float scale, pa_dtype q_dtype,
+                                 int32_t partition_tokens, void* workspace,
+                                 size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_chunked_prefill over an MXFP4 cache: the same operation, arguments, limits,
+ * workspace (pa_chunked_prefill_workspace_size with PA_MXFP4) and run-time
+ * table errors; q_dtype F16 or BF16. Keys and values enter the products as
+ * q_dtype values, as pa_gather_cache_mxfp4 gives them, but that with an F16
+ * query scales of more than 2^13 (b > 140) are taken as 2^13 and those below
+ * 2^-24 (b < 103) as 0: exact for caches written from F16 rows but for codes
+ * below F16's own resolution; a BF16 query takes every value exactly. A NaN
+ * block makes NaN what it belongs to (a V block: its 32 outputs) in every row
+ * of a tile of query rows that reads it, masked or not.
+ */
+PA_API pa_status pa_chunked_prefill_mxfp4(
+    void* out, const void* query, const int32_t* cu_query_lens, int32_t num_tokens,
+    int32_t max_query_len, const uint8_t* key_cache, const uint8_t* value_cache,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
+    int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int64_t num_blocks, float scale, pa_dtype q_dtype, void* workspace,
+    size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Forking sequences and compacting the pool, over all planes of a cache.      */
+/* ------------------------------------------------------------------------- */
+/*
+ * A plane is one tensor whose first axis is the block: the key or the value
+ * cache of a layer, or one of the four planes of an MXFP4 cache. All planes of
+ * a call have the same number of blocks; block_bytes is the contiguous size of
+ * one block, a positive multiple of 16 (at most 2 GiB), base is 16-byte
+ * aligned device memory. The planes array is host memory, read during the call.
+ */
+typedef struct pa_plane {
+  void* base;
+  int64_t block_bytes;
+} pa_plane;
+
+/*
+ * Fork sequences (parallel samples, beams; [P4] shares the blocks of a prompt
+ * among samples under a reference count). Child i of parent p = parents[i]
+ * (a row of block_tables) gets
+ *   new_context_lens[i] = context_lens[p]
+ *   new_block_tables[i] = p's entries for ceil(context_lens[p] / block_size)
+ *                         blocks, -1 after them;
+ * when the last block is not full and fresh_blocks[i] >= 0, that block is
+ * copied into block fresh_blocks[i] in every plane, and the child's entry names
+ * it; with fresh_blocks[i] < 0 the child shares it (the one child that carries
+ * its parent on, or one that will be copied on write). A full last block is
+ * shared and fresh_blocks[i] is not used. The reference counts are the host
+ * allocator's (pa_alloc_fork).
+ * block_tables      device int32 [num_seqs, max_blocks_per_seq]
+ * context_lens      device int32 [num_seqs]
+ * parents, fresh_blocks  device int32 [num_children]; a parent may be named
+ *                   many times; the fresh blocks are distinct and no parent's.
+ * new_block_tables  device int32 [num_children, max_blocks_per_seq] (written;
+ *                   does not overlap block_tables)
+ * new_context_lens  device int32 [num_children] (written; no overlap with
+ *                   context_lens)
+ * error_word        optional device int32: bit 32 is set for a parent that is
+ *                   no sequence (its child gets length 0 and no blocks), bit 1
+ *                   for a block id outside the pool (nothing is copied; a fresh
+ *                   id outside it leaves the entry -1), bit 2 for a context
+ *                   length outside its table row (clipped).
+ * num_planes may be 0 (tables only).
+ */
+PA_API pa_status pa_fork_sequences(const pa_plane* planes, int32_t num_planes, int64_t num_blocks,
+                                   int32_t block_size, const int32_t* block_tables,
+                                   int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* parents,
+                                   const int32_t* fresh_blocks, int32_t num_children,
+                                   int32_t* new_block_tables, int32_t* new_context_lens,
+                                   int32_t* error_word, pa_stream_t stream);
+
+/*
+ * Move blocks together: for each move i, block moves[2i] is copied to block
+ * moves[2i+1] in every plane, and every entry of block_tables that names a
+ * moved block names its new place. The sources ascend, the destinations are
+ * distinct and none of them is a source (pa_alloc_compact makes such a list);
+ * entries that name no moved block stay as they are, -1 included.
+ * moves             device int32 [num_moves][2]
+ * block_tables      device int32, num_entries entries in all (or NULL and 0)
+ * error_word        optional device int32: bit 1 is set for a move with an id
+ *                   outside the pool (it is left out, entries too), bit 64 for
+ *                   sources that do not ascend or a destination that is a
+ *                   source (the result is then unspecified).
+ */
+PA_API pa_status pa_compact_blocks(const pa_plane* planes, int32_t num_planes, int64_t num_blocks,
+                                   const int32_t* moves, int32_t num_moves, int32_t* block_tables,
+                                   int64_t num_entries, int32_t* error_word, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Block content hashes for prefix caching (host only).                        */
 /* ------------------------------------------------------------------------- */
 
@@ -400,6 +555,26 @@ PA_API pa_status pa_alloc_free(pa_alloc* a, const int32_t* ids, int32_t n);
  * PA_ERR_INVALID_ARG for a free or unknown id. */
 PA_API pa_status pa_alloc_copy_on_write(pa_alloc* a, int32_t id, int32_t* id_out,
                                         int32_t* must_copy);
+/* num_children children of a sequence with the n blocks ids (in order), whose
+ * last block is not full when partial_tail is nonzero: every block but a
+ * partial last one gains num_children references, and fresh_out[i] is the
+ * block that child i's copy of the last one goes to (-1 when it is full, and
+ * shared). All-or-nothing: PA_ERR_OOM when the fresh blocks do not fit,
+ * PA_ERR_INVALID_ARG for a block that is not allocated. An id may be listed
+ * more than once (it gains as many references each time). */
+PA_API pa_status pa_alloc_fork(pa_alloc* a, const int32_t* ids, int32_t n, int32_t partial_tail,
+                               int32_t num_children, int32_t* fresh_out);
+/* Move the allocated blocks to the front of the pool: with L of them, every
+ * allocated id >= L moves to a free id < L. moves_out[2i], moves_out[2i+1] is
+ * the i-th move (both ascend), *num_moves their number; references and
+ * registered hashes go with the block, a cached block that a move lands on
+ * loses its hash, and the ids left behind go to the back of the free list in
+ * ascending order. The caller copies the blocks (pa_compact_blocks) before
+ * anything is written to the pool again. With room for fewer moves than there
+ * are (cap), nothing changes and PA_ERR_INVALID_ARG is returned with their
+ * number in *num_moves. */
+PA_API pa_status pa_alloc_compact(pa_alloc* a, int32_t* moves_out, int32_t cap,
+                                  int32_t* num_moves);
 /* Prefix caching ([P4] Prefix Caching: prefix blocks are reused across
  * requests, recognised by hash matching). hashes: n 32-byte block hashes
  * (pa_prompt_block_hashes), in prompt order. Each hash that names a cached

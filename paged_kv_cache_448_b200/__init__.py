@@ -8,6 +8,10 @@ only. If the library is missing the first op raises ``ImportError``.
 Ops:
   * ``reshape_and_cache`` — scatter a step's new K/V rows into cache slots.
   * ``decode`` — paged attention of one query token per sequence.
+  * ``reshape_and_cache_mxfp4``, ``gather_cache_mxfp4``, ``decode_mxfp4``,
+    ``chunked_prefill_mxfp4`` — the same over a cache held in 4 bits (MXFP4).
+  * ``CachePool`` — forking sequences (parallel samples, beams) and compacting
+    the pool over all planes of a cache.
   * ``BlockAllocator``, ``build_block_table``, ``build_slot_mapping`` — host
     allocator and integer-table builders (no GPU).
 """
@@ -18,7 +22,7 @@ import ctypes
 import numpy as np
 
 from . import _native
-from ._native import PagedError, check
+from ._native import PA_BF16, PA_F16, PA_FP8_E4M3, PA_MXFP4, PagedError, check
 
 __all__ = ["reshape_and_cache", "decode", "decode_noalloc", "decode_noalloc_check",
            "inject_wait_timeout", "decode_workspace",
@@ -27,7 +31,10 @@ __all__ = ["reshape_and_cache", "decode", "decode_noalloc", "decode_noalloc_chec
            "chunked_prefill_workspace", "chunked_prefill_workspace_size", "copy_blocks", "sha256", "block_hash",
            "prompt_block_hashes", "BlockAllocator",
            "build_block_table",
-           "build_slot_mapping", "PagedError", "dtype_code"]
+           "build_slot_mapping", "PagedError", "dtype_code",
+           "PA_F16", "PA_BF16", "PA_FP8_E4M3", "PA_MXFP4",
+           "mxfp4_cache", "reshape_and_cache_mxfp4", "gather_cache_mxfp4", "decode_mxfp4",
+           "chunked_prefill_mxfp4", "CachePool"]
 
 
 def dtype_code(t) -> int:
@@ -226,6 +233,252 @@ def copy_blocks(src_key_cache, src_value_cache, dst_key_cache, dst_value_cache, 
         _ptr(error_word), _stream_handle(stream)))
 
 
+# ---------------------------------------------------------------- 4-bit cache
+
+def _call(fn, at, stream, *args) -> None:
+    """fn(*args, stream handle) with the device of tensor `at` current; without
+    a stream, that device's current one."""
+    import torch
+    if not at.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if at.device.index == torch.cuda.current_device():
+        check(fn(*args, _stream_handle(stream)))
+    else:
+        with torch.cuda.device(at.device):
+            check(fn(*args, _stream_handle(stream)))
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(at, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != at.device:
+            raise ValueError(f"tensors on different devices ({at.device} and {t.device})")
+
+
+def _row_tensor(t, name: str) -> None:
+    _need(dtype_code(t) in (PA_F16, PA_BF16) and t.dim() == 3 and t.is_contiguous(),
+          f"{name} must be a contiguous f16 or bf16 [tokens, heads, head_dim] tensor")
+
+
+def _int_tensor(t, shape, name: str) -> None:
+    import torch
+    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _table_tensor(t, rows, name: str) -> None:
+    import torch
+    _need(t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous() and
+          rows in (None, t.shape[0]),
+          f"{name} must be a contiguous int32 [{'rows' if rows is None else rows}, "
+          "max_blocks_per_seq] tensor")
+
+
+def _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, head_dim):
+    """(num_blocks, num_kv_heads, block_size) of an MXFP4 cache's planes."""
+    import torch
+    _need(key_cache.dim() == 4, "key_cache must be [num_blocks, num_kv_heads, block_size, "
+                                "head_dim / 2]")
+    NB, Hkv, BS = key_cache.shape[:3]
+    for t, width, name in ((key_cache, head_dim // 2, "key_cache"),
+                           (value_cache, head_dim // 2, "value_cache"),
+                           (k_scales, head_dim // 32, "k_scales"),
+                           (v_scales, head_dim // 32, "v_scales")):
+        _need(t.dtype == torch.uint8 and t.is_contiguous() and
+              tuple(t.shape) == (NB, Hkv, BS, width),
+              f"{name} must be a contiguous uint8 tensor of shape {[NB, Hkv, BS, width]}")
+    return NB, Hkv, BS
+
+
+def mxfp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
+    """The four planes of an empty MXFP4 cache, zeros: (key_cache, value_cache) uint8
+    [num_blocks, num_kv_heads, block_size, head_dim / 2] and (k_scales, v_scales)
+    uint8 [num_blocks, num_kv_heads, block_size, head_dim / 32]."""
+    import torch
+    return tuple(torch.zeros((num_blocks, num_kv_heads, block_size, w), dtype=torch.uint8,
+                             device=device)
+                 for w in (head_dim // 2, head_dim // 2, head_dim // 32, head_dim // 32))
+
+
+def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales,
+                            slot_mapping, *, stream=None) -> None:
+    """reshape_and_cache into an MXFP4 cache (pa_reshape_and_cache_mxfp4): key/value
+    [T, Hkv, D] f16|bf16, planes as mxfp4_cache makes them, slot_mapping int32 [T]
+    (negative = skip)."""
+    _row_tensor(key, "key")
+    _need(value.shape == key.shape and value.dtype == key.dtype and value.is_contiguous(),
+          "value must be contiguous, of key's shape and dtype")
+    T, Hkv, D = key.shape
+    NB, heads, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
+    _need(heads == Hkv, f"the cache has {heads} kv-heads, key {Hkv}")
+    _int_tensor(slot_mapping, (T,), "slot_mapping")
+    _same_device(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping)
+    _call(_native.lib().pa_reshape_and_cache_mxfp4, key, stream, _ptr(key), _ptr(value),
+          _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
+          _ptr(slot_mapping), T, Hkv, D, BS, NB, dtype_code(key))
+
+
+def gather_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, *,
+                       stream=None) -> None:
+    """Rows of an MXFP4 cache by slot into key/value [T, Hkv, D] f16|bf16
+    (pa_gather_cache_mxfp4); rows whose slot is negative or outside the pool stay
+    as they were."""
+    _row_tensor(key, "key")
+    _need(value.shape == key.shape and value.dtype == key.dtype and value.is_contiguous(),
+          "value must be contiguous, of key's shape and dtype")
+    T, Hkv, D = key.shape
+    NB, heads, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
+    _need(heads == Hkv, f"the cache has {heads} kv-heads, key {Hkv}")
+    _int_tensor(slot_mapping, (T,), "slot_mapping")
+    _same_device(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping)
+    _call(_native.lib().pa_gather_cache_mxfp4, key, stream, _ptr(key), _ptr(value),
+          _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
+          _ptr(slot_mapping), T, Hkv, D, BS, NB, dtype_code(key))
+
+
+def _workspace_for(at, stream, make):
+    """A workspace of the call's own on `at`'s device, kept alive for `stream`."""
+    import torch
+    with torch.cuda.device(at.device):
+        ws = make()
+        if stream is not None:
+            ws.record_stream(stream)
+    return ws
+
+
+def _check_workspace(ws) -> None:
+    import torch
+    _need(ws.dtype == torch.uint8 and ws.is_contiguous(), "workspace must be a contiguous uint8 "
+                                                          "tensor")
+
+
+def decode_mxfp4(out, query, key_cache, value_cache, k_scales, v_scales, block_tables,
+                 context_lens, max_context_len: int, scale: float, *, partition_tokens: int = 0,
+                 workspace=None, stream=None):
+    """decode over an MXFP4 cache (pa_decode_mxfp4): out/query [S, H, D] f16|bf16, planes as
+    mxfp4_cache makes them; workspace from decode_workspace(..., cache_dtype=PA_MXFP4).
+    Returns ``out``."""
+    _row_tensor(query, "query")
+    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+          "out must be contiguous, of query's shape and dtype")
+    S, H, D = query.shape
+    NB, Hkv, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
+    _table_tensor(block_tables, S, "block_tables")
+    _int_tensor(context_lens, (S,), "context_lens")
+    if workspace is None:
+        workspace = _workspace_for(query, stream, lambda: decode_workspace(
+            S, H, Hkv, D, BS, max_context_len, partition_tokens, device=query.device,
+            stream=stream, cache_dtype=PA_MXFP4))
+    _check_workspace(workspace)
+    _same_device(query, out, key_cache, value_cache, k_scales, v_scales, block_tables,
+                 context_lens, workspace)
+    _call(_native.lib().pa_decode_mxfp4, query, stream, _ptr(out), _ptr(query), _ptr(key_cache),
+          _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
+          block_tables.shape[1], _ptr(context_lens), int(max_context_len), S, H, Hkv, D, BS, NB,
+          float(scale), dtype_code(query), int(partition_tokens), _ptr(workspace),
+          workspace.numel())
+    return out
+
+
+def chunked_prefill_mxfp4(out, query, cu_query_lens, max_query_len: int, key_cache, value_cache,
+                          k_scales, v_scales, block_tables, context_lens, max_context_len: int,
+                          scale: float, *, workspace=None, stream=None):
+    """chunked_prefill over an MXFP4 cache (pa_chunked_prefill_mxfp4): out/query [T, H, D]
+    f16|bf16, planes as mxfp4_cache makes them; workspace from
+    chunked_prefill_workspace(..., PA_MXFP4). Returns ``out``."""
+    _row_tensor(query, "query")
+    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+          "out must be contiguous, of query's shape and dtype")
+    T, H, D = query.shape
+    S = context_lens.shape[0]
+    NB, Hkv, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
+    _table_tensor(block_tables, S, "block_tables")
+    _int_tensor(context_lens, (S,), "context_lens")
+    _int_tensor(cu_query_lens, (S + 1,), "cu_query_lens")
+    if workspace is None:
+        workspace = _workspace_for(query, stream, lambda: chunked_prefill_workspace(
+            S, T, H, Hkv, D, max_query_len, max_context_len, PA_MXFP4, device=query.device,
+            stream=stream))
+    _check_workspace(workspace)
+    _same_device(query, out, key_cache, value_cache, k_scales, v_scales, block_tables,
+                 context_lens, cu_query_lens, workspace)
+    _call(_native.lib().pa_chunked_prefill_mxfp4, query, stream, _ptr(out), _ptr(query),
+          _ptr(cu_query_lens), T, int(max_query_len), _ptr(key_cache), _ptr(value_cache),
+          _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
+          _ptr(context_lens), int(max_context_len), S, H, Hkv, D, BS, NB, float(scale),
+          dtype_code(query), _ptr(workspace), workspace.numel())
+    return out
+
+
+# ---------------------------------------------------------------- pages of a cache
+
+class CachePool:
+    """The planes of a paged cache, for operations on whole blocks of all of them.
+
+    planes: tensors [num_blocks, ...] on one device, contiguous, of any dtype and block
+    size (a multiple of 16 bytes): the key and value caches of every layer, or their
+    codes and scales. The pool keeps a reference to each.
+    """
+
+    def __init__(self, planes, block_size: int):
+        planes = list(planes)
+        _need(len(planes) > 0, "a pool has at least one plane")
+        first = planes[0]
+        for t in planes:
+            _need(t.dim() >= 2 and t.is_contiguous() and t.shape[0] == first.shape[0] and
+                  t.shape[0] > 0,
+                  "planes must be contiguous [num_blocks, ...] tensors of as many blocks")
+        _need(first.is_cuda, "planes must be on a CUDA device")
+        _same_device(first, *planes)
+        self.planes = planes
+        self.block_size = int(block_size)
+        self.num_blocks = int(first.shape[0])
+        self._array = (_native.Plane * len(planes))(
+            *[_native.Plane(t.data_ptr(), t[0].numel() * t.element_size()) for t in planes])
+
+    def fork(self, block_tables, context_lens, parents, fresh_blocks, new_block_tables,
+             new_context_lens, *, error_word=None, stream=None) -> None:
+        """Children of sequences (pa_fork_sequences): child i of row parents[i] shares its
+        parent's whole blocks; a last block that is not full is copied into block
+        fresh_blocks[i] of every plane (a negative entry shares it). Writes
+        new_block_tables int32 [n, max_blocks_per_seq] and new_context_lens int32 [n]."""
+        _table_tensor(block_tables, None, "block_tables")
+        S, width = block_tables.shape
+        _int_tensor(context_lens, (S,), "context_lens")
+        n = parents.shape[0] if parents.dim() == 1 else -1
+        _int_tensor(parents, (n,), "parents")
+        _int_tensor(fresh_blocks, (n,), "fresh_blocks")
+        _int_tensor(new_block_tables, (n, width), "new_block_tables")
+        _int_tensor(new_context_lens, (n,), "new_context_lens")
+        if error_word is not None:
+            _int_tensor(error_word, (1,), "error_word")
+        _same_device(self.planes[0], block_tables, context_lens, parents, fresh_blocks,
+                     new_block_tables, new_context_lens, error_word)
+        _call(_native.lib().pa_fork_sequences, self.planes[0], stream, self._array,
+              len(self.planes), self.num_blocks, self.block_size, _ptr(block_tables), S, width,
+              _ptr(context_lens), _ptr(parents), _ptr(fresh_blocks), n, _ptr(new_block_tables),
+              _ptr(new_context_lens), _ptr(error_word))
+
+    def compact(self, moves, block_tables=None, *, error_word=None, stream=None) -> None:
+        """Move blocks moves[i, 0] -> moves[i, 1] in every plane and rename them in
+        block_tables, in place (pa_compact_blocks; BlockAllocator.compact makes the list)."""
+        _need(moves.dim() == 2, "moves must be a contiguous int32 [n, 2] tensor")
+        _int_tensor(moves, (moves.shape[0], 2), "moves")
+        if block_tables is not None:
+            _table_tensor(block_tables, None, "block_tables")
+        if error_word is not None:
+            _int_tensor(error_word, (1,), "error_word")
+        _same_device(self.planes[0], moves, block_tables, error_word)
+        _call(_native.lib().pa_compact_blocks, self.planes[0], stream, self._array,
+              len(self.planes), self.num_blocks, _ptr(moves), moves.shape[0],
+              _ptr(block_tables), 0 if block_tables is None else block_tables.numel(),
+              _ptr(error_word))
+
+
 def sha256(data: bytes) -> bytes:
     """SHA-256 of a byte string (pa_sha256)."""
     buf = ctypes.create_string_buffer(bytes(data), max(len(data), 1))
@@ -291,6 +544,24 @@ class BlockAllocator:
         check(self._lib.pa_alloc_copy_on_write(self._h, int(block_id), ctypes.byref(out),
                                                ctypes.byref(copy)))
         return int(out.value), bool(copy.value)
+
+    def fork(self, ids, partial_tail: bool, num_children: int) -> list:
+        """References of num_children children on a sequence's blocks; the fresh block of
+        each child's last block when that is not full, -1 otherwise (pa_alloc_fork)."""
+        a = _i32(ids)
+        out = np.empty(max(num_children, 1), np.int32)
+        check(self._lib.pa_alloc_fork(self._h, a.ctypes.data if a.size else None, a.size,
+                                      int(bool(partial_tail)), num_children, out.ctypes.data))
+        return [int(i) for i in out[:num_children]]
+
+    def compact(self) -> np.ndarray:
+        """int32 [n, 2]: moves (from, to) that bring the allocated blocks to the front of
+        the pool; the allocator has made them, the caller copies (pa_alloc_compact)."""
+        moves = np.empty((max(self.num_blocks - self.num_free, 1), 2), np.int32)
+        n = ctypes.c_int32()
+        check(self._lib.pa_alloc_compact(self._h, moves.ctypes.data, len(moves),
+                                         ctypes.byref(n)))
+        return moves[:n.value].copy()
 
     def acquire_prefix(self, hashes):
         """Blocks for a prompt's full-block hashes ([n, 32] uint8): cached ones

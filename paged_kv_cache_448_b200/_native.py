@@ -12,7 +12,7 @@ import threading
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpaged.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OOM, PA_ERR_CUDA, PA_ERR_BAD_TABLE = range(6)
-PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_MXFP4 = 0, 1, 2, 3
 
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_OOM",
                 4: "PA_ERR_CUDA", 5: "PA_ERR_BAD_TABLE"}
@@ -40,6 +40,18 @@ SIGNATURES = [
     ("pa_workspace_init", _st, [_P, _sz, _P]),
     ("pa_inject_wait_timeout", _st, [_i32, ctypes.c_uint64]),
     ("pa_copy_blocks", _st, [_P, _P, _P, _P, _P, _i32, _i64, _i64, _i64, _P, _P]),
+    ("pa_reshape_and_cache_mxfp4", _st, [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32,
+                                         _i64, _st, _P]),
+    ("pa_gather_cache_mxfp4", _st, [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i64,
+                                    _st, _P]),
+    ("pa_decode_mxfp4", _st, [_P, _P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _i32,
+                              _i32, _i32, _i64, _f32, _st, _i32, _P, _sz, _P]),
+    ("pa_chunked_prefill_mxfp4", _st, [_P, _P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P,
+                                       _i32, _i32, _i32, _i32, _i32, _i32, _i64, _f32, _st, _P,
+                                       _sz, _P]),
+    ("pa_fork_sequences", _st, [_P, _i32, _i64, _i32, _P, _i32, _i32, _P, _P, _P, _i32, _P, _P,
+                                _P, _P]),
+    ("pa_compact_blocks", _st, [_P, _i32, _i64, _P, _i32, _P, _i64, _P, _P]),
     ("pa_sha256", _st, [_P, _i64, _P]),
     ("pa_block_hash", _st, [_P, _P, _i32, _P]),
     ("pa_prompt_block_hashes", _st, [_P, _i64, _i32, _P]),
@@ -49,6 +61,8 @@ SIGNATURES = [
     ("pa_alloc_share", _st, [_P, _i32]),
     ("pa_alloc_free", _st, [_P, _P, _i32]),
     ("pa_alloc_copy_on_write", _st, [_P, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
+    ("pa_alloc_fork", _st, [_P, _P, _i32, _i32, _i32, _P]),
+    ("pa_alloc_compact", _st, [_P, _P, _i32, ctypes.POINTER(_i32)]),
     ("pa_alloc_acquire_prefix", _st, [_P, _P, _i32, _P, ctypes.POINTER(_i32)]),
     ("pa_alloc_register_hash", _st, [_P, _i32, _P]),
     ("pa_alloc_lookup", _i32, [_P, _P]),
@@ -59,6 +73,12 @@ SIGNATURES = [
     ("pa_build_block_table", _st, [_P, _P, _i32, _i32, _P]),
     ("pa_build_slot_mapping", _st, [_P, _i32, _i32, _P, _P, _i32, _i32, _P]),
 ]
+
+
+class Plane(ctypes.Structure):
+    """pa_plane: one tensor whose first axis is the block."""
+    _fields_ = [("base", ctypes.c_void_p), ("block_bytes", ctypes.c_int64)]
+
 
 _lock = threading.Lock()
 _lib = None

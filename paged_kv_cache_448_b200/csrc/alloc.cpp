@@ -162,6 +162,67 @@ PA_API pa_status pa_alloc_copy_on_write(pa_alloc* a, int32_t id, int32_t* id_out
   return PA_OK;
 }
 
+PA_API pa_status pa_alloc_fork(pa_alloc* a, const int32_t* ids, int32_t n, int32_t partial_tail,
+                               int32_t num_children, int32_t* fresh_out) {
+  clear_error();
+  if (!a || n < 0 || (n > 0 && !ids) || num_children < 0 || (num_children > 0 && !fresh_out) ||
+      (partial_tail && n == 0))
+    return fail(PA_ERR_INVALID_ARG, "alloc_fork: bad args");
+  const int32_t shared = partial_tail ? n - 1 : n;
+  for (int32_t i = 0; i < n; ++i)
+    if (ids[i] < 0 || static_cast<size_t>(ids[i]) >= a->refcount.size() ||
+        a->refcount[ids[i]] == 0)
+      return fail(PA_ERR_INVALID_ARG, "alloc_fork: block %d is not allocated", ids[i]);
+  if (partial_tail && static_cast<size_t>(num_children) > a->free_list.size())
+    return fail(PA_ERR_OOM, "Need %d blocks, only %zu available", num_children,
+                a->free_list.size());
+  for (int32_t i = 0; i < shared; ++i) {
+    if (a->refcount[ids[i]] > INT32_MAX - num_children) {
+      for (int32_t j = 0; j < i; ++j) a->refcount[ids[j]] -= num_children;
+      return fail(PA_ERR_INVALID_ARG, "alloc_fork: refcount overflow");
+    }
+    a->refcount[ids[i]] += num_children;
+  }
+  for (int32_t i = 0; i < num_children; ++i) fresh_out[i] = partial_tail ? a->pop_free() : -1;
+  return PA_OK;
+}
+
+PA_API pa_status pa_alloc_compact(pa_alloc* a, int32_t* moves_out, int32_t cap,
+                                  int32_t* num_moves) {
+  clear_error();
+  if (!a || cap < 0 || (cap > 0 && !moves_out) || !num_moves)
+    return fail(PA_ERR_INVALID_ARG, "alloc_compact: bad args");
+  const int32_t nb = static_cast<int32_t>(a->refcount.size());
+  const int32_t live = nb - static_cast<int32_t>(a->free_list.size());
+  int32_t k = 0;
+  for (int32_t id = live; id < nb; ++id) k += a->refcount[id] > 0;
+  *num_moves = k;
+  if (k > cap)
+    return fail(PA_ERR_INVALID_ARG, "alloc_compact: %d moves, room for %d", k, cap);
+  int32_t hole = 0, n = 0;
+  for (int32_t id = live; id < nb; ++id) {
+    if (a->refcount[id] == 0) continue;
+    while (a->refcount[hole] > 0) ++hole;  // there are as many holes below `live`
+    // the hole's place in the free list becomes that of the id left behind
+    a->free_list.splice(a->free_list.end(), a->free_list, a->where[hole]);
+    *a->where[hole] = id;
+    a->where[id] = a->where[hole];
+    a->drop_hash(hole);
+    a->refcount[hole] = a->refcount[id];
+    a->refcount[id] = 0;
+    if (a->hashed[id]) {
+      a->hashed[hole] = 1;
+      a->hash_of[hole] = a->hash_of[id];
+      a->by_hash[a->hash_of[id]] = hole;
+      a->hashed[id] = 0;
+    }
+    moves_out[2 * n] = id;
+    moves_out[2 * n + 1] = hole;
+    ++n;
+  }
+  return PA_OK;
+}
+
 PA_API pa_status pa_alloc_acquire_prefix(pa_alloc* a, const uint8_t* hashes, int32_t n,
                                          int32_t* ids_out, int32_t* num_hits) {
   clear_error();

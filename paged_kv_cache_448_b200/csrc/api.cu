@@ -12,6 +12,7 @@
 
 #include "decode_args.h"
 #include "device_common.cuh"
+#include "pages.h"
 #include "prefill_args.h"
 #include "paged.h"
 #include "status.h"
@@ -89,6 +90,59 @@ pa_status encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_bloc
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
   return PA_OK;
+}
+
+// Tensor maps over an MXFP4 cache (mxfp4.cuh). Codes: [num_blocks][kv-heads x
+// block_size rows][head_dim / 2 bytes], one box = one kv-head's rows of a block,
+// swizzled by the row's width. Scales: [num_blocks][kv-heads x block_size x
+// head_dim / 32 bytes], one box = the bytes of one kv-head.
+pa_status encode_mxfp4_codes(CUtensorMap* map, const void* codes, int64_t num_blocks,
+                             int32_t block_size, int32_t hkv, int32_t head_dim) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t rb = static_cast<cuuint64_t>(head_dim) / 2;
+  const cuuint64_t rows = static_cast<cuuint64_t>(hkv) * block_size;
+  cuuint64_t dims[3] = {rb, rows, static_cast<cuuint64_t>(num_blocks)};
+  cuuint64_t strides[2] = {rb, rb * rows};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(rb), static_cast<cuuint32_t>(block_size), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return PA_OK;
+}
+
+pa_status encode_mxfp4_scales(CUtensorMap* map, const void* scales, int64_t num_blocks,
+                              int32_t block_size, int32_t hkv, int32_t head_dim) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t per_head = static_cast<cuuint32_t>(block_size) * (head_dim / 32);
+  const cuuint64_t per_block = static_cast<cuuint64_t>(hkv) * per_head;
+  cuuint64_t dims[2] = {per_block, static_cast<cuuint64_t>(num_blocks)};
+  cuuint64_t strides[1] = {per_block};
+  cuuint32_t box[2] = {per_head, 1u};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(scales), dims,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return PA_OK;
+}
+
+// All four planes of an MXFP4 cache: K codes, V codes, K scales, V scales.
+pa_status encode_mxfp4(CUtensorMap (&maps)[4], const uint8_t* kc, const uint8_t* vc,
+                       const uint8_t* ks, const uint8_t* vs, int64_t num_blocks,
+                       int32_t block_size, int32_t hkv, int32_t head_dim) {
+  pa_status st = encode_mxfp4_codes(&maps[0], kc, num_blocks, block_size, hkv, head_dim);
+  if (st == PA_OK)
+    st = encode_mxfp4_codes(&maps[1], vc, num_blocks, block_size, hkv, head_dim);
+  if (st == PA_OK)
+    st = encode_mxfp4_scales(&maps[2], ks, num_blocks, block_size, hkv, head_dim);
+  if (st == PA_OK)
+    st = encode_mxfp4_scales(&maps[3], vs, num_blocks, block_size, hkv, head_dim);
+  return st;
 }
 
 pa_status cuda_status(cudaError_t e, const char* what) {
@@ -491,6 +545,8 @@ namespace {
 // tcgen05 kernel, or about four waves of three mma.sync CTAs per SM, the
 // tiles of each CTA are cut into parts of at least 256 tokens (16 tiles, whole
 // steps of the kernel) handled by separate CTAs and merged by a combine kernel.
+// An MXFP4 cache always runs on tcgen05, whose converter warps widen a code
+// once for all of a CTA's rows.
 struct PrefillPlan {
   bool tc;                  // tcgen05 kernel (rows on M), else mma.sync
   int32_t q_tiles, partition_tiles, max_parts;
@@ -498,7 +554,8 @@ struct PrefillPlan {
 
 PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t group,
                               int32_t head_dim, int32_t max_query_len, int32_t max_context_len,
-                              bool fp8) {
+                              pa_dtype cache_dtype) {
+  const bool fp8 = cache_dtype == PA_FP8_E4M3;
   PrefillPlan p{};
   const int64_t rows = static_cast<int64_t>(max_query_len) * group;
 
@@ -507,8 +564,9 @@ PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t gr
   const int32_t qt_tc = (rows >= 256 ? 256 : 128) / group;
   const int64_t tc_ctas = static_cast<int64_t>(num_seqs) * num_kv_heads *
                           ((max_query_len + qt_tc - 1) / qt_tc);
-  p.tc = (!fp8 || head_dim == 128) &&
-         (rows >= 128 || (rows >= 8 && tc_ctas >= 2LL * sm_count()));
+  p.tc = cache_dtype == PA_MXFP4 ||
+         ((!fp8 || head_dim == 128) &&
+          (rows >= 128 || (rows >= 8 && tc_ctas >= 2LL * sm_count())));
   const int32_t qt = p.tc ? qt_tc : prefill_tokens_per_cta(group);
   p.q_tiles = (max_query_len + qt - 1) / qt;
   const int32_t max_tiles = std::max<int32_t>(1, (max_context_len + 15) / 16);
@@ -553,11 +611,12 @@ PA_API size_t pa_chunked_prefill_workspace_size(int32_t num_seqs, int32_t num_to
                                                 int32_t max_context_len, pa_dtype cache_dtype) {
   if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_query_len < 0 || max_context_len < 0 || num_heads % num_kv_heads != 0 ||
-      (cache_dtype != PA_F16 && cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3))
+      (cache_dtype != PA_F16 && cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3 &&
+       cache_dtype != PA_MXFP4))
     return 0;
   const PrefillPlan p = make_prefill_plan(num_seqs, num_kv_heads, num_heads / num_kv_heads,
                                           head_dim, max_query_len, max_context_len,
-                                          cache_dtype == PA_FP8_E4M3);
+                                          cache_dtype);
   return prefill_workspace_bytes(p, num_tokens, num_heads, head_dim);
 }
 
@@ -612,7 +671,7 @@ PA_API pa_status pa_chunked_prefill(void* out, const void* query, const int32_t*
   CUtensorMap kmap, vmap;
   const PrefillPlan plan =
       make_prefill_plan(num_seqs, num_kv_heads, group, head_dim, max_query_len,
-                        max_context_len, fp8);
+                        max_context_len, cache_dtype);
   const bool tc = plan.tc;   // the tcgen05 kernel takes one-segment boxes
   const size_t need = prefill_workspace_bytes(plan, num_tokens, num_heads, head_dim);
   if (workspace_bytes < need)
@@ -661,6 +720,352 @@ PA_API pa_status pa_chunked_prefill(void* out, const void* query, const int32_t*
       tc ? launch_prefill_tc(a, kmap, vmap, qd, cd, head_dim, group, max_query_len, cs)
          : launch_prefill(a, kmap, vmap, qd, cd, head_dim, group, max_query_len, cs);
   return cuda_status(e, "chunked_prefill");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- MXFP4 cache
+
+namespace paged {
+namespace {
+
+// Sizes and pointers that the row copies into and out of an MXFP4 cache check.
+pa_status check_mxfp4_rows(const char* what, const void* key, const void* value,
+                           const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
+                           const uint8_t* vs, const int32_t* slots, int32_t num_tokens,
+                           int32_t hkv, int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                           pa_dtype kv_dtype) {
+  if (num_tokens < 0 || hkv <= 0 || num_blocks <= 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: negative or zero size", what);
+  if (!shape_supported(head_dim, block_size))
+    return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d / block_size %d unsupported", what, head_dim,
+                block_size);
+  if (kv_dtype != PA_F16 && kv_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "%s: rows must be f16 or bf16", what);
+  if (static_cast<int64_t>(num_tokens) * hkv * (head_dim / 8) / 256 >= INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: too many rows for one launch", what);
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !kc || !vc || !ks || !vs || !slots)
+    return fail(PA_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(kc, 16) || !aligned(vc, 16) ||
+      !aligned(ks, 16) || !aligned(vs, 16) || !aligned(slots, 4))
+    return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace paged
+
+extern "C" {
+
+PA_API pa_status pa_reshape_and_cache_mxfp4(const void* key, const void* value, uint8_t* key_cache,
+                                            uint8_t* value_cache, uint8_t* k_scales,
+                                            uint8_t* v_scales, const int32_t* slot_mapping,
+                                            int32_t num_tokens, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size,
+                                            int64_t num_blocks, pa_dtype kv_dtype,
+                                            pa_stream_t stream) {
+  clear_error();
+  pa_status st = check_mxfp4_rows("reshape_and_cache_mxfp4", key, value, key_cache, value_cache,
+                                  k_scales, v_scales, slot_mapping, num_tokens, num_kv_heads,
+                                  head_dim, block_size, num_blocks, kv_dtype);
+  if (st != PA_OK || num_tokens == 0) return st;
+  return cuda_status(
+      launch_mxfp4_write(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping,
+                         num_tokens, num_kv_heads, head_dim, block_size, num_blocks,
+                         kv_dtype == PA_F16 ? kF16 : kBF16,
+                         reinterpret_cast<cudaStream_t>(stream)),
+      "reshape_and_cache_mxfp4");
+}
+
+PA_API pa_status pa_gather_cache_mxfp4(void* key, void* value, const uint8_t* key_cache,
+                                       const uint8_t* value_cache, const uint8_t* k_scales,
+                                       const uint8_t* v_scales, const int32_t* slot_mapping,
+                                       int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int64_t num_blocks, pa_dtype kv_dtype,
+                                       pa_stream_t stream) {
+  clear_error();
+  pa_status st = check_mxfp4_rows("gather_cache_mxfp4", key, value, key_cache, value_cache,
+                                  k_scales, v_scales, slot_mapping, num_tokens, num_kv_heads,
+                                  head_dim, block_size, num_blocks, kv_dtype);
+  if (st != PA_OK || num_tokens == 0) return st;
+  return cuda_status(
+      launch_mxfp4_read(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping,
+                        num_tokens, num_kv_heads, head_dim, block_size, num_blocks,
+                        kv_dtype == PA_F16 ? kF16 : kBF16,
+                        reinterpret_cast<cudaStream_t>(stream)),
+      "gather_cache_mxfp4");
+}
+
+PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* key_cache,
+                                 const uint8_t* value_cache, const uint8_t* k_scales,
+                                 const uint8_t* v_scales, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 int64_t num_blocks, float scale, pa_dtype q_dtype,
+                                 int32_t partition_tokens, void* workspace,
+                                 size_t workspace_bytes, pa_stream_t stream) {
+  clear_error();
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 ||
+      max_context_len < 0 || num_blocks <= 0 || partition_tokens < 0)
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: negative or zero size");
+  if (num_heads % num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: num_heads %% num_kv_heads != 0");
+  const int32_t group = num_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8)
+    return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: query group %d not in {1,2,4,8}", group);
+  if (!shape_supported(head_dim, block_size))
+    return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: head_dim %d / block_size %d unsupported",
+                head_dim, block_size);
+  if (q_dtype != PA_F16 && q_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: query must be f16 or bf16");
+  if (num_blocks > INT32_MAX || static_cast<int64_t>(num_kv_heads) * block_size > INT32_MAX / 4)
+    return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: pool or block too large");
+  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: scale is not finite");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: workspace missing or not 256-byte aligned");
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !block_tables ||
+      !context_lens)
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: null pointer");
+  if (!aligned(out, 16) || !aligned(query, 16) || !aligned(key_cache, 16) ||
+      !aligned(value_cache, 16) || !aligned(k_scales, 16) || !aligned(v_scales, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: misaligned pointer");
+
+  const Plan plan = make_plan(num_seqs, num_kv_heads, block_size, max_context_len,
+                              partition_tokens, false);
+  if (num_seqs > 65535 || plan.max_parts > kMaxParts)
+    return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: %d sequences x %d partitions exceed the grid",
+                num_seqs, plan.max_parts);
+  const Layout lay = layout_for(plan, num_seqs, num_heads, head_dim);
+  if (workspace_bytes < lay.total)
+    return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: workspace %zu bytes < %zu needed",
+                workspace_bytes, lay.total);
+  CUtensorMap maps[4];
+  pa_status st = encode_mxfp4(maps, key_cache, value_cache, k_scales, v_scales, num_blocks,
+                              block_size, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+
+  DecodeArgs a{};
+  a.out = out;
+  a.query = query;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.err = reinterpret_cast<int32_t*>(ws) + kWordError;
+  a.diag = reinterpret_cast<int32_t*>(ws) + kWordDiag;
+  if (plan.max_parts > 1) {
+    a.ws_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    a.ws_o = reinterpret_cast<float*>(ws + lay.o);
+  }
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.ctx_limit = std::min<int64_t>(max_context_len,
+                                  static_cast<int64_t>(max_blocks_per_seq) * block_size);
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.partition_blocks = plan.partition_blocks;
+  a.max_parts = plan.max_parts;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.block_size = block_size;
+  take_injection(&a.skip_tile, &a.wait_limit_ns);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int qd = q_dtype == PA_F16 ? kF16 : kBF16;
+  st = cuda_status(decode_mxfp4(a, maps, qd, head_dim, cs), "decode_mxfp4");
+  if (st != PA_OK || plan.max_parts <= 1) return st;
+  return cuda_status(launch_reduce(a, qd, head_dim, cs), "decode_mxfp4 combine");
+}
+
+PA_API pa_status pa_chunked_prefill_mxfp4(
+    void* out, const void* query, const int32_t* cu_query_lens, int32_t num_tokens,
+    int32_t max_query_len, const uint8_t* key_cache, const uint8_t* value_cache,
+    const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
+    int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int64_t num_blocks, float scale, pa_dtype q_dtype, void* workspace,
+    size_t workspace_bytes, pa_stream_t stream) {
+  clear_error();
+  if (num_tokens < 0 || max_query_len < 0 || num_seqs < 0 || num_heads <= 0 ||
+      num_kv_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || num_blocks <= 0)
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: negative or zero size");
+  if (num_heads % num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: num_heads %% num_kv_heads != 0");
+  const int32_t group = num_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8)
+    return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: query group %d not in {1,2,4,8}",
+                group);
+  if (!shape_supported(head_dim, block_size))
+    return fail(PA_ERR_UNSUPPORTED,
+                "chunked_prefill_mxfp4: head_dim %d / block_size %d unsupported", head_dim,
+                block_size);
+  if (q_dtype != PA_F16 && q_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: query must be f16 or bf16");
+  if (num_blocks > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: pool too large");
+  if (num_seqs > 65535 || num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED,
+                "chunked_prefill_mxfp4: more than 65535 sequences or kv-heads");
+  if (!std::isfinite(scale))
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: scale is not finite");
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kHeaderBytes)
+    return fail(PA_ERR_INVALID_ARG,
+                "chunked_prefill_mxfp4: workspace missing, small or misaligned");
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !block_tables ||
+      !context_lens || !cu_query_lens)
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: null pointer");
+  if (!aligned(out, 16) || !aligned(query, 16) || !aligned(key_cache, 16) ||
+      !aligned(value_cache, 16) || !aligned(k_scales, 16) || !aligned(v_scales, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(cu_query_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: misaligned pointer");
+  const PrefillPlan plan = make_prefill_plan(num_seqs, num_kv_heads, group, head_dim,
+                                             max_query_len, max_context_len, PA_MXFP4);
+  const size_t need = prefill_workspace_bytes(plan, num_tokens, num_heads, head_dim);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID_ARG, "chunked_prefill_mxfp4: workspace %zu bytes < %zu needed",
+                workspace_bytes, need);
+  PrefillArgs a{};
+  a.out = out;
+  a.query = query;
+  a.cu_query_lens = cu_query_lens;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.err = reinterpret_cast<int32_t*>(workspace) + kWordError;
+  a.diag = reinterpret_cast<int32_t*>(workspace) + kWordDiag;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.ctx_limit = std::min<int64_t>(max_context_len,
+                                  static_cast<int64_t>(max_blocks_per_seq) * block_size);
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q_tiles = plan.q_tiles;
+  a.partition_tiles = plan.partition_tiles;
+  a.max_parts = plan.max_parts;
+  take_injection(&a.skip_tile, &a.wait_limit_ns);
+  if (plan.max_parts > 1) {
+    const size_t rows = static_cast<size_t>(num_tokens) * num_heads * plan.max_parts;
+    a.ws_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+    a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                      align256(kHeaderBytes + rows * sizeof(float2)));
+  }
+  return cuda_status(
+      launch_prefill_mxfp4(a, {key_cache, value_cache, k_scales, v_scales},
+                           q_dtype == PA_F16 ? kF16 : kBF16, head_dim, group, max_query_len,
+                           reinterpret_cast<cudaStream_t>(stream)),
+      "chunked_prefill_mxfp4");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ page operators
+
+namespace paged {
+namespace {
+
+bool overlap(const void* p, int64_t pn, const void* q, int64_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + static_cast<uintptr_t>(qn) && b < a + static_cast<uintptr_t>(pn);
+}
+
+pa_status check_planes(const char* what, const pa_plane* planes, int32_t num_planes,
+                       int64_t num_blocks) {
+  if (num_planes < 0 || num_blocks <= 0 || num_blocks > INT32_MAX)
+    return fail(PA_ERR_INVALID_ARG, "%s: negative or zero size", what);
+  if (num_planes > 0 && !planes) return fail(PA_ERR_INVALID_ARG, "%s: null pointer", what);
+  int64_t items = 0;
+  for (int32_t i = 0; i < num_planes; ++i) {
+    if (!planes[i].base) return fail(PA_ERR_INVALID_ARG, "%s: null plane %d", what, i);
+    if (!aligned(planes[i].base, 16))
+      return fail(PA_ERR_INVALID_ARG, "%s: misaligned plane %d", what, i);
+    if (planes[i].block_bytes <= 0 || planes[i].block_bytes % 16 != 0)
+      return fail(PA_ERR_INVALID_ARG, "%s: block_bytes of plane %d is no positive multiple of 16",
+                  what, i);
+    items += planes[i].block_bytes / 4096 + 1;
+    if (planes[i].block_bytes > INT32_MAX || items > INT32_MAX / 2)
+      return fail(PA_ERR_UNSUPPORTED, "%s: blocks of more than 2 GiB", what);
+  }
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace paged
+
+extern "C" {
+
+PA_API pa_status pa_fork_sequences(const pa_plane* planes, int32_t num_planes, int64_t num_blocks,
+                                   int32_t block_size, const int32_t* block_tables,
+                                   int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* parents,
+                                   const int32_t* fresh_blocks, int32_t num_children,
+                                   int32_t* new_block_tables, int32_t* new_context_lens,
+                                   int32_t* error_word, pa_stream_t stream) {
+  clear_error();
+  if (block_size <= 0 || num_seqs <= 0 || max_blocks_per_seq <= 0 || num_children < 0)
+    return fail(PA_ERR_INVALID_ARG, "fork_sequences: negative or zero size");
+  pa_status st = check_planes("fork_sequences", planes, num_planes, num_blocks);
+  if (st != PA_OK) return st;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "fork_sequences: table rows of more than 2^31 tokens");
+  if (num_children == 0) return PA_OK;
+  if (!block_tables || !context_lens || !parents || !fresh_blocks || !new_block_tables ||
+      !new_context_lens)
+    return fail(PA_ERR_INVALID_ARG, "fork_sequences: null pointer");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(parents, 4) ||
+      !aligned(fresh_blocks, 4) || !aligned(new_block_tables, 4) ||
+      !aligned(new_context_lens, 4) || !aligned(error_word, 4))
+    return fail(PA_ERR_INVALID_ARG, "fork_sequences: misaligned pointer");
+  const int64_t row = 4LL * max_blocks_per_seq, n = num_children;
+  if (overlap(block_tables, row * num_seqs, new_block_tables, row * n) ||
+      overlap(context_lens, 4LL * num_seqs, new_context_lens, 4 * n))
+    return fail(PA_ERR_INVALID_ARG, "fork_sequences: the new tables overlap the old ones");
+  ForkArgs a{};
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.parents = parents;
+  a.fresh_blocks = fresh_blocks;
+  a.new_block_tables = new_block_tables;
+  a.new_context_lens = new_context_lens;
+  a.err = error_word;
+  a.num_blocks = num_blocks;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_children = num_children;
+  a.block_size = block_size;
+  static_assert(sizeof(pa_plane) == sizeof(PlaneRef), "the same layout");
+  return cuda_status(launch_fork(a, reinterpret_cast<const PlaneRef*>(planes), num_planes,
+                                 sm_count(), reinterpret_cast<cudaStream_t>(stream)),
+                     "fork_sequences");
+}
+
+PA_API pa_status pa_compact_blocks(const pa_plane* planes, int32_t num_planes, int64_t num_blocks,
+                                   const int32_t* moves, int32_t num_moves, int32_t* block_tables,
+                                   int64_t num_entries, int32_t* error_word, pa_stream_t stream) {
+  clear_error();
+  if (num_moves < 0 || num_entries < 0)
+    return fail(PA_ERR_INVALID_ARG, "compact_blocks: negative size");
+  pa_status st = check_planes("compact_blocks", planes, num_planes, num_blocks);
+  if (st != PA_OK) return st;
+  if (num_moves == 0) return PA_OK;
+  if (!moves || (num_entries > 0 && !block_tables))
+    return fail(PA_ERR_INVALID_ARG, "compact_blocks: null pointer");
+  if (!aligned(moves, 8) || !aligned(block_tables, 4) || !aligned(error_word, 4))
+    return fail(PA_ERR_INVALID_ARG, "compact_blocks: misaligned pointer");
+  CompactArgs a{};
+  a.moves = moves;
+  a.block_tables = block_tables;
+  a.err = error_word;
+  a.num_blocks = num_blocks;
+  a.num_entries = num_entries;
+  a.num_moves = num_moves;
+  return cuda_status(launch_compact(a, reinterpret_cast<const PlaneRef*>(planes), num_planes,
+                                    sm_count(), reinterpret_cast<cudaStream_t>(stream)),
+                     "compact_blocks");
 }
 
 }  // extern "C"

@@ -16,6 +16,8 @@ enum : int32_t {
   kErrWaitTimeout = 4,     // a pipeline wait gave up (never expected)
   kErrBadSlot = 8,         // reshape_and_cache: a slot outside the pool
   kErrQueryLonger = 16,    // multi-token query: more query rows than context (rows are zeros)
+  kErrBadParent = 32,      // fork: a parent that is no sequence (the child is empty)
+  kErrBadMoves = 64,       // compact: sources not ascending, or a destination that is a source
 };
 
 // Failure sites recorded in the diagnostic words (the first word of the record).
@@ -84,6 +86,22 @@ cudaError_t decode_fp8_tc(const DecodeArgs& a, const CUtensorMap& kmap, const CU
                           int q_dtype, int group, cudaStream_t stream);
 // kv-heads per CTA of that kernel (its TMA boxes span as many heads).
 int decode_fp8_tc_heads_per_cta(int num_kv_heads, int group);
+
+// Decode over an MXFP4 cache; maps: K codes, V codes, K scales, V scales.
+cudaError_t decode_mxfp4(const DecodeArgs& a, const CUtensorMap (&maps)[4], int q_dtype,
+                         int head_dim, cudaStream_t stream);
+
+// Rows of 16-bit values into / out of an MXFP4 cache, by slot.
+cudaError_t launch_mxfp4_write(const void* key, const void* value, uint8_t* kc, uint8_t* vc,
+                               uint8_t* ks, uint8_t* vs, const int32_t* slots,
+                               int32_t num_tokens, int32_t hkv, int32_t head_dim,
+                               int32_t block_size, int64_t num_blocks, int kv_dtype,
+                               cudaStream_t stream);
+cudaError_t launch_mxfp4_read(void* key, void* value, const uint8_t* kc, const uint8_t* vc,
+                              const uint8_t* ks, const uint8_t* vs, const int32_t* slots,
+                              int32_t num_tokens, int32_t hkv, int32_t head_dim,
+                              int32_t block_size, int64_t num_blocks, int kv_dtype,
+                              cudaStream_t stream);
 
 cudaError_t launch_reshape_and_cache(const void* key, const void* value, void* key_cache,
                                      void* value_cache, const int32_t* slot_mapping,

@@ -1,0 +1,796 @@
+// decode_mxfp4.cu — decode over a 4-bit (MXFP4) paged cache.
+//
+// For each (sequence, query head): out = sum_t softmax_t(scale q . K_t) V_t
+// over the context, K_t and V_t being code * 2^(b - 127) per 32-element block
+// (mxfp4.cuh). One CTA per (kv-head, sequence, partition); each warp owns
+// every NW-th step of 32 tokens and streams it through its own ring of
+// shared-memory stages (per cache block one TMA box of K codes, K scales, V
+// codes, V scales; 136 bytes a token and kv-head at head_dim 128).
+//
+// Arithmetic on a step, per warp, on mma.sync m16n8k16 (f16 in, fp32
+// accumulators) with the tokens (S) or the dims (O) on M and the group's
+// query heads on N:
+//  * ldmatrix hands lane (g, c) [g = lane / 4, c = lane % 4] word c of the 16
+//    bytes a block of token g has: 8 codes, dims 32 b + 8 c .. + 7. One
+//    conversion instruction per byte makes the f16 pair that A wants (every
+//    E2M1 value is an f16 value). The contraction order within a block is
+//    permuted to match, in the query fragments too, and every MMA stays inside
+//    one block, so the block's scale is applied to the fp32 partial sums:
+//      S[t, h] = sum_b 2^(bK[t, b] - 127) (codes . q)_b.
+//  * ldmatrix.trans of the same bytes gives lane (g, c) the codes of dims
+//    32 b + 4 g .. + 3 for tokens 2 c and 2 c + 1, the A operand of V^T P once
+//    the two tokens' codes are interleaved. The V scale belongs to the
+//    contracted index, so it multiplies P, per block of dims:
+//      O[d, h] += V~[t, d] (P[t, h] 2^(bV[t, b(d)] - r_b)),
+//    r_b being a running reference for the block's scales (undone at the end)
+//    that keeps the product within f16.
+// P and O follow a base-2 online softmax whose maximum m moves only when a
+// logit passes it by more than 8, so P <= 2^8; r_b moves only when a scale
+// passes it by more than 7, so P 2^(bV - r_b) <= 2^15 < 65504. Scales more
+// than 8 below r_b would lose P's low bits, or all of it: a step that holds
+// one takes its tokens band by band (15 powers of two each, relative to the
+// band's largest scale) and adds the bands in fp32. All three conditions are
+// checked with one vote per step; the slow paths run a few times a unit.
+// A probability is rounded to f16 (2^-12 relative) before the product with V;
+// sums, maxima, logits and O are fp32.
+// A bf16 query row is scaled by a power of two that puts its largest element
+// in [1, 2) and held in f16: exact for elements down to 2^-17 of the largest,
+// an error of at most 2^-25 of it below.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "consumer_mma.cuh"
+#include "decode_args.h"
+#include "decode_kernel.cuh"
+#include "device_common.cuh"
+#include "mxfp4.cuh"
+
+namespace paged {
+namespace {
+
+constexpr int kStep = 32;  // tokens per step
+
+template <int D_, int NW_>
+struct MxCfg {
+  static constexpr int D = D_, NW = NW_;
+  static constexpr int RB = D / 2;                    // code bytes of a row
+  static constexpr int SB = D / 32;                   // scale bytes of a row = blocks
+  static constexpr int CODES = kStep * RB;            // K (or V) codes of a step
+  static constexpr int SCALES = 256;  // K (or V) scales of a step: a 128-byte slot per box
+  static constexpr int SWZ = RB == 64 ? 0x30 : 0x10;  // TMA 64-byte / 32-byte swizzle
+  static constexpr int R = 3;                         // stages of a warp's ring
+  static constexpr int STAGE = 2 * CODES;             // K codes, V codes
+  static constexpr int SSTAGE = 2 * SCALES;           // K scales, V scales
+  static constexpr int OFF_S = NW * R * STAGE;
+  static constexpr int OFF_BAR = OFF_S + NW * R * SSTAGE;
+  static constexpr int OFF_IDS = OFF_BAR + 8 * NW * R;
+  static_assert(NW * 8 * (D + 1) * 4 + NW * 16 * 4 <= NW * R * STAGE, "merge buffer fits");
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit values held one pair a lane.
+__device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float fast_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 2^n, 0 below the normal numbers.
+__device__ __forceinline__ float pow2i(int n) {
+  return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
+}
+
+// Each 16-bit half v of x where lo <= v <= hi, the other halves as 0.
+__device__ __forceinline__ uint32_t halves_within(uint32_t x, int lo, int hi) {
+  const int a = static_cast<int>(x & 0xffffu), b = static_cast<int>(x >> 16);
+  return (a >= lo && a <= hi ? x & 0x0000ffffu : 0u) | (b >= lo && b <= hi ? x & 0xffff0000u : 0u);
+}
+
+// f16 of 2^(v - r) for each 16-bit half v of x, r - 14 <= v <= r + 15: its
+// exponent field is v - r + 15 (exact in integer arithmetic on the word).
+__device__ __forceinline__ uint32_t f16_pow2(uint32_t x, int r) {
+  return x * 0x400u + static_cast<uint32_t>(15 - r) * 0x04000400u;
+}
+
+// Nonzero if some byte of w is 255.
+__device__ __forceinline__ uint32_t has_ff(uint32_t w) {
+  return (~w - 0x01010101u) & w & 0x80808080u;
+}
+
+// The TMA box of one block: its rows of one kv-head (codes), or the scales of
+// those rows. Coordinates: byte within the row, row (or byte) within the
+// block, block.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar)),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
+// The attention state of one warp: query heads 2c and 2c+1 of lane (g, c),
+// tokens shared out over g.
+template <class QF, int D>
+struct MxState {
+  static constexpr int NB = D / 32;  // blocks of a row
+  uint32_t q[NB][4];   // query fragments: block b, k-step i: q[b][2 i], q[b][2 i + 1]
+  float qs[2];         // base-2 logit scale of the two heads
+  float m[2], l[2];    // running maximum; this lane's part of the sum
+  float o[NB][2][4];   // O: block b, dims 32 b + 4 g + 2 i (+1) x heads 2c, 2c+1
+  int ref[NB];         // r_b: scale byte the V scales are taken relative to (-1: none yet)
+  uint32_t nan_blocks; // blocks of V with a NaN scale in the context
+  bool low;            // a reference so low that the window below it holds the byte 0
+
+  __device__ __forceinline__ void init(const DecodeArgs& a, const uint8_t* query, int group,
+                                       int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    const uint4* row = reinterpret_cast<const uint4*>(query + static_cast<int64_t>(g) * D * 2);
+    uint4 w[NB];
+    float mq = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      w[b] = g < group ? row[b * 4 + c] : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (std::is_same<QF, BF16>::value) {
+        const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = cvt2(BF16{}, x[j]);
+          mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    }
+    int e = 0;  // power of two of this row (head g)
+    if constexpr (std::is_same<QF, BF16>::value) {
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+      if (mq > 0.f && isfinite(mq)) e = -max(ilogbf(mq), -126);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (std::is_same<QF, BF16>::value) {
+          const float2 f = cvt2(BF16{}, x[j]);
+          const __half2 h = __floats2half2_rn(ldexpf(f.x, e), ldexpf(f.y, e));
+          q[b][j] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          q[b][j] = x[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int eh = __shfl_sync(0xffffffffu, e, (2 * c + i) * 4);
+      // -e is undone in two factors, each a normal number
+      qs[i] = a.scale_log2 * ldexpf(1.f, -(eh / 2)) * ldexpf(1.f, eh / 2 - eh);
+      m[i] = -CUDART_INF_F;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      ref[b] = -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[b][i][j] = 0.f;
+    }
+    nan_blocks = 0u;
+    low = true;
+  }
+
+  // The NB scale bytes of a row.
+  static __device__ __forceinline__ uint32_t scale_word(const uint8_t* p) {
+    if constexpr (NB == 4) return *reinterpret_cast<const uint32_t*>(p);
+    return *reinterpret_cast<const uint16_t*>(p);
+  }
+  static __device__ __forceinline__ int byte_of(uint32_t w, int b) { return (w >> (8 * b)) & 255; }
+
+  // One step: kStep rows of codes at kc / vc (swizzled), scales at ks / vs
+  // (those of rows 16 and up `half` bytes further); rows from `valid` on are
+  // not of the context and may hold anything.
+  template <int SWZ>
+  __device__ __forceinline__ void step(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
+                                       const uint8_t* vs, int half, int valid, int lane) {
+    constexpr int RB = D / 2, SB = NB;
+    constexpr unsigned FULL = 0xffffffffu;
+    const int g = lane >> 2, c = lane & 3;
+    // ---- logits: x[u][i][j] = token 16 u + 8 i + g, head 2 c + j
+    float x[2][2][2];
+    uint32_t ff = 0u;  // a K scale of 255 among this lane's tokens
+    uint32_t kw[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t r[2][NB];  // [rows g / g + 8][block]
+      if constexpr (NB == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int off = (16 * u + 8 * i + (lane & 7)) * RB + (lane >> 3) * 16;
+          ldsm_x4(kc + (off ^ ((off >> 3) & SWZ)), r[i]);
+        }
+      } else {
+        uint32_t t[4];
+        const int off = (16 * u + 8 * (lane >> 4) + (lane & 7)) * RB + ((lane >> 3) & 1) * 16;
+        ldsm_x4(kc + (off ^ ((off >> 3) & SWZ)), t);
+        r[0][0] = t[0];
+        r[0][1] = t[1];
+        r[1][0] = t[2];
+        r[1][1] = t[3];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kw[u][i] = scale_word(ks + u * half + (8 * i + g) * SB);
+        if (valid < kStep && 16 * u + 8 * i + g >= valid) kw[u][i] = 0u;
+        ff |= has_ff(kw[u][i]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) x[u][i][j] = 0.f;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t h0[4], h1[4];
+        mx_unpack8(r[0][b], h0);
+        mx_unpack8(r[1][b], h1);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(s, h0[0], h1[0], h0[1], h1[1], q[b][0], q[b][1]);
+        mma16816(s, h0[2], h1[2], h0[3], h1[3], q[b][2], q[b][3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f =
+              __uint_as_float((b == 3 ? kw[u][i] >> 1 : kw[u][i] << (23 - 8 * b)) & 0x7f800000u);
+          x[u][i][0] = fmaf(f, s[2 * i], x[u][i][0]);
+          x[u][i][1] = fmaf(f, s[2 * i + 1], x[u][i][1]);
+        }
+      }
+    }
+    // ---- scales of V: words of tokens 16 u + 8 i + 2 c, + 1
+    uint32_t vw[2][2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* p = vs + u * half + (8 * i + 2 * c) * SB;
+        if constexpr (NB == 4) {
+          const uint2 t = *reinterpret_cast<const uint2*>(p);
+          vw[u][i][0] = t.x;
+          vw[u][i][1] = t.y;
+        } else {
+          const uint32_t t = *reinterpret_cast<const uint32_t*>(p);
+          vw[u][i][0] = t & 0xffffu;
+          vw[u][i][1] = t >> 16;
+        }
+      }
+    if (valid < kStep) {  // the last step of a unit
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (16 * u + 8 * i + 2 * c + j >= valid) vw[u][i][j] = 0u;
+          }
+    }
+    // exponent of 2^(bV - r_b) as an f16 exponent field, two tokens a word:
+    // bytes of blocks 0, 2 and 1, 3 as 16-bit halves, paired over the tokens
+    uint32_t ex[2][2][NB];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t e0 = vw[u][i][0] & 0x00ff00ffu, e1 = vw[u][i][1] & 0x00ff00ffu;
+        const uint32_t o0 = (vw[u][i][0] >> 8) & 0x00ff00ffu,
+                       o1 = (vw[u][i][1] >> 8) & 0x00ff00ffu;
+        ex[u][i][0] = prmt(e0, e1, 0x5410);
+        ex[u][i][1] = prmt(o0, o1, 0x5410);
+        if constexpr (NB == 4) {
+          ex[u][i][2] = prmt(e0, e1, 0x7632);
+          ex[u][i][3] = prmt(o0, o1, 0x7632);
+        }
+      }
+    float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float t = x[u][i][j] * qs[j];
+          if (valid < kStep && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
+          x[u][i][j] = t;
+          mx[j] = fmaxf(mx[j], t);
+        }
+    if (valid < kStep) {  // rows that are not of the context: a scale within the window
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int t = valid - (16 * u + 8 * i + 2 * c);  // rows of this word that are
+            const uint32_t keep = t <= 0 ? 0u : t == 1 ? 0x0000ffffu : 0xffffffffu;
+            ex[u][i][b] = (ex[u][i][b] & keep) |
+                          (static_cast<uint32_t>(max(ref[b], 1)) * 0x10001u & ~keep);
+          }
+    }
+    const bool lift =
+        mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || outside(ex) || ff;
+    bool wide = low;  // V scales below the window (the same in every lane)
+    if (__any_sync(FULL, lift)) {
+      update(x, mx, kw, ff, vw, ex);
+      wide = low || __any_sync(FULL, outside(ex));
+    }
+    // ---- probabilities, their sum, and P as B operand (tokens x heads)
+    const float mu0 = m[0] == -CUDART_INF_F ? 0.f : m[0];
+    const float mu1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+    uint32_t p[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float p0 = fast_ex2(x[u][i][0] - mu0), p1 = fast_ex2(x[u][i][1] - mu1);
+        l[0] += p0;
+        l[1] += p1;
+        const __half2 h = __floats2half2_rn(p0, p1);
+        p[u][i] = movm_trans(*reinterpret_cast<const uint32_t*>(&h));
+      }
+    // ---- O += V^T (P 2^(bV - r))
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t r[2][NB];
+      if constexpr (NB == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int off = (16 * u + 8 * i + (lane & 7)) * RB + (lane >> 3) * 16;
+          ldsm_x4_trans(vc + (off ^ ((off >> 3) & SWZ)), r[i]);
+        }
+      } else {
+        uint32_t t[4];
+        const int off = (16 * u + 8 * (lane >> 4) + (lane & 7)) * RB + ((lane >> 3) & 1) * 16;
+        ldsm_x4_trans(vc + (off ^ ((off >> 3) & SWZ)), t);
+        r[0][0] = t[0];
+        r[0][1] = t[1];
+        r[1][0] = t[2];
+        r[1][1] = t[3];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t f0 = f16_pow2(ex[u][0][b], ref[b]), f1 = f16_pow2(ex[u][1][b], ref[b]);
+        if (wide) {  // tokens outside the window weigh nothing here
+          f0 = weights(ex[u][0][b], ref[b], 8);
+          f1 = weights(ex[u][1][b], ref[b], 8);
+        }
+        uint32_t h[2][4];
+        v_pairs(r[0][b], h[0]);
+        v_pairs(r[1][b], h[1]);
+        const uint32_t b0 = hmul2u(p[u][0], f0), b1 = hmul2u(p[u][1], f1);
+        mma16816(o[b][0], h[0][0], h[0][1], h[1][0], h[1][1], b0, b1);
+        mma16816(o[b][1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
+      }
+    }
+    if (wide) bands<SWZ>(vc, p, ex, lane);
+  }
+
+  // Nonzero if some V scale of the step (exponents of ex) is not within
+  // [r_b - 8, r_b + 7] of its block's reference.
+  __device__ __forceinline__ uint32_t outside(const uint32_t (&ex)[2][2][NB]) const {
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      // halves 0x8000 + (v - r + 8): no carry between them, 0x800x within the window
+      const uint32_t add = static_cast<uint32_t>(0x8000 + 8 - ref[b]) * 0x10001u;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) bits |= (ex[u][i][b] + add) ^ 0x80008000u;
+    }
+    return bits & 0xfff0fff0u;
+  }
+
+  // f16 of 2^(v - r) for the halves v of x with max(r - below, 1) <= v <= r + 7,
+  // 0 for the others (a scale byte of 0 reads as 0).
+  static __device__ __forceinline__ uint32_t weights(uint32_t x, int r, int below) {
+    const int lo = max(r - below, 1);
+    const uint32_t in = halves_within(x, lo, r + 7);
+    const uint32_t keep = ((in & 0xffffu) ? 0x0000ffffu : 0u) | ((in >> 16) ? 0xffff0000u : 0u);
+    // the halves left out take the value r first: no carry into the other half
+    return f16_pow2(in | (static_cast<uint32_t>(max(r, 0)) * 0x10001u & ~keep), max(r, 0)) & keep;
+  }
+
+  // One word of V codes as ldmatrix.trans gives it (dims 4 g .. + 3 of tokens
+  // 2 c, 2 c + 1) -> per dim the f16 pair of the two tokens.
+  static __device__ __forceinline__ void v_pairs(uint32_t w, uint32_t (&h)[4]) {
+    // bytes: (token 2c, token 2c + 1) codes of dims 0, 2 and of dims 1, 3
+    const uint32_t t0 = (w & 0x0f0fu) | ((w >> 12) & 0xf0f0u);
+    const uint32_t t1 = ((w >> 4) & 0x0f0fu) | ((w >> 16) & 0xf0f0u);
+    uint32_t t[4];
+    mx_unpack8(prmt(t0, t1, 0x5410), t);
+    h[0] = t[0];
+    h[2] = t[1];
+    h[1] = t[2];
+    h[3] = t[3];
+  }
+
+  // The step's tokens whose V scale lies below the window of its block: bands
+  // of 15 powers of two from the largest such scale down, each a product of
+  // its own added to O in fp32.
+  template <int SWZ>
+  __device__ __forceinline__ void bands(const uint8_t* vc, const uint32_t (&p)[2][2],
+                                        const uint32_t (&ex)[2][2][NB], int lane) {
+    constexpr int RB = D / 2;
+    constexpr unsigned FULL = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      int hi = ref[b] - 9;
+      while (hi > 0) {  // the same in every lane
+        int t = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t in = halves_within(ex[u][i][b], 1, hi);
+            t = max(t, max(static_cast<int>(in & 0xffffu), static_cast<int>(in >> 16)));
+          }
+        t = max(t, __shfl_xor_sync(FULL, t, 1));
+        t = max(t, __shfl_xor_sync(FULL, t, 2));
+        if (t == 0) break;
+        float add[2][4] = {};
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          // 16 rows x the 16 bytes of this block, transposed
+          uint32_t r[4];
+          const int off = (16 * u + (lane & 15)) * RB + b * 16;
+          ldsm_x4_trans(vc + (off ^ ((off >> 3) & SWZ)), r);
+          uint32_t h[2][4];
+          v_pairs(r[0], h[0]);
+          v_pairs(r[1], h[1]);
+          const uint32_t e0 = u ? ex[1][0][b] : ex[0][0][b], e1 = u ? ex[1][1][b] : ex[0][1][b];
+          const uint32_t p0 = u ? p[1][0] : p[0][0], p1 = u ? p[1][1] : p[0][1];
+          const uint32_t b0 = hmul2u(p0, weights(halves_within(e0, 1, t), t, 14));
+          const uint32_t b1 = hmul2u(p1, weights(halves_within(e1, 1, t), t, 14));
+          mma16816(add[0], h[0][0], h[0][1], h[1][0], h[1][1], b0, b1);
+          mma16816(add[1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
+        }
+        const float f = pow2i(t - ref[b]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[b][i][j] = fmaf(add[i][j], f, o[b][i][j]);
+        hi = t - 15;
+      }
+    }
+  }
+
+  // The scale references move to the largest V scale of the step; a NaN scale
+  // is remembered for its block.
+  __device__ __forceinline__ void update_scales(const uint32_t (&vw)[2][2][2],
+                                                uint32_t (&ex)[2][2][NB]) {
+    constexpr unsigned FULL = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      int t = -1;
+      bool bad = false;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int v = byte_of(vw[u][i][j], b);
+            if (v == kMxNan) {
+              bad = true;
+              ex[u][i][b] &= j ? 0x0000ffffu : 0xffff0000u;  // as 0: no weight
+            } else {
+              t = max(t, v);
+            }
+          }
+      t = max(t, __shfl_xor_sync(FULL, t, 1));
+      t = max(t, __shfl_xor_sync(FULL, t, 2));
+      if (__any_sync(FULL, bad)) nan_blocks |= 1u << b;
+      t = min(t, 247);  // 248 .. 254 stay within the 7 powers of two above r_b
+      if (t > ref[b]) {
+        const float f = ref[b] < 0 ? 0.f : pow2i(ref[b] - t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[b][i][j] *= f;
+        ref[b] = t;
+      }
+    }
+    low = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) low |= ref[b] <= 8;
+  }
+
+  // A maximum or a scale reference has to move, or a scale is NaN (a K scale:
+  // the token's logit is NaN for every head).
+  __device__ __forceinline__ void update(float (&x)[2][2][2], float (&mx)[2],
+                                         const uint32_t (&kw)[2][2], uint32_t ff,
+                                         const uint32_t (&vw)[2][2][2],
+                                         uint32_t (&ex)[2][2][NB]) {
+    constexpr unsigned FULL = 0xffffffffu;
+    if (ff) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (has_ff(kw[u][i])) x[u][i][0] = x[u][i][1] = CUDART_NAN_F;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) mx[j] = fmaxf(mx[j], __shfl_xor_sync(FULL, mx[j], d));
+      if (mx[j] > m[j]) {
+        const float f = m[j] == -CUDART_INF_F ? 0.f : fast_ex2(m[j] - mx[j]);
+        l[j] *= f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o[b][i][j] *= f;
+            o[b][i][2 + j] *= f;
+          }
+        m[j] = mx[j];
+      }
+    }
+    update_scales(vw, ex);
+  }
+
+  // (m, l) of each head and O in true units to shared memory.
+  __device__ __forceinline__ void finish(float* ml, float* ob, int group, int lane) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[j] += __shfl_xor_sync(FULL, l[j], d);
+      if (g == 0 && 2 * c + j < group) {
+        ml[2 * (2 * c + j)] = m[j];
+        ml[2 * (2 * c + j) + 1] = l[j];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float f = nan_blocks >> b & 1 ? CUDART_NAN_F
+                      : ref[b] <= 0       ? 0.f
+                                          : pow2i(ref[b] - 127);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int head = 2 * c + j, dim = 32 * b + 4 * g + 2 * i + k;
+            if (head < group) ob[head * D + dim] = o[b][i][2 * k + j] * f;
+          }
+    }
+  }
+};
+
+template <class QF, int D, int NW>
+__global__ void __launch_bounds__(NW * 32)
+    paged_decode_mxfp4_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+                              const __grid_constant__ CUtensorMap vmap,
+                              const __grid_constant__ CUtensorMap ksmap,
+                              const __grid_constant__ CUtensorMap vsmap) {
+  using C = MxCfg<D, NW>;
+  constexpr int R = C::R;
+  constexpr unsigned FULL = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  int32_t* ids = reinterpret_cast<int32_t*>(smem + C::OFF_IDS);
+  __shared__ int aborted;
+
+  const int kvh = blockIdx.x, s = blockIdx.y, part = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.num_heads / a.num_kv_heads;
+  if (lane == 0) {
+    for (int r = 0; r < R; ++r) mbar_init(&bars[warp * R + r], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    aborted = 0;
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&ksmap);
+    prefetch_tensormap(&vsmap);
+  }
+  // everything below reads what earlier kernels of the stream wrote
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  int ctx = a.context_lens[s];
+  if (ctx > a.ctx_limit || ctx < 0) {
+    if (threadIdx.x == 0 && part == 0) report(a.err, kErrContextClipped);
+    ctx = ctx < 0 ? 0 : a.ctx_limit;
+  }
+  const int bs = a.block_size;
+  const int nblk = (ctx + bs - 1) / bs;
+  const int parts = nblk == 0 ? 1 : (nblk + a.partition_blocks - 1) / a.partition_blocks;
+  if (part >= parts) return;
+  const int b_begin = part * a.partition_blocks;
+  const int nlocal = min(b_begin + a.partition_blocks, nblk) - b_begin;
+  const int tokens = max(0, min(ctx, (b_begin + nlocal) * bs) - b_begin * bs);
+  const int nsteps = (tokens + kStep - 1) / kStep;
+
+  // block ids of this unit -> shared memory, validated once
+  const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  for (int i = threadIdx.x; i < nlocal; i += NW * 32) {
+    int32_t id = table[b_begin + i];
+    if (id < 0 || id >= a.num_blocks) {
+      report(a.err, kErrBadBlockId);
+      id = -1;  // a box outside the pool: zero codes and scales
+    }
+    ids[i] = id;
+  }
+  __syncthreads();
+
+  const int my_count = nsteps > warp ? (nsteps - warp + NW - 1) / NW : 0;
+  uint8_t* my_codes = smem + warp * R * C::STAGE;
+  uint8_t* my_scales = smem + C::OFF_S + warp * R * C::SSTAGE;
+  uint64_t* my_bars = bars + warp * R;
+  const uint64_t policy = l2_policy_evict_first();
+
+  const int half = bs == 16 ? 128 : 16 * C::SB;  // from the scales of row 15 to those of row 16
+  auto issue = [&](int k) {  // k-th step of this warp
+    const int t0 = (warp + k * NW) * kStep;
+    const int stage = k % R;
+    const int blk0 = t0 / bs, n = min(nlocal - blk0, kStep / bs);
+    mbar_arrive_expect_tx(&my_bars[stage], static_cast<uint32_t>(n * bs * 2 * (C::RB + C::SB)));
+    uint8_t* codes = my_codes + stage * C::STAGE;
+    uint8_t* scales = my_scales + stage * C::SSTAGE;
+    for (int j = 0; j < n; ++j) {
+      // a failure-detection test leaves out the block that holds its tile
+      const int tile0 = (t0 + j * bs) / kTileRows;
+      if (a.skip_tile >= tile0 && a.skip_tile < tile0 + bs / kTileRows &&
+          skip_for_test(a.skip_tile, a.skip_tile))
+        continue;
+      const int32_t id = ids[blk0 + j];
+      tma_load_3d(codes + j * bs * C::RB, &kmap, &my_bars[stage], 0, kvh * bs, id, policy);
+      tma_load_2d(scales + j * 128, &ksmap, &my_bars[stage], kvh * bs * C::SB, id, policy);
+      tma_load_3d(codes + C::CODES + j * bs * C::RB, &vmap, &my_bars[stage], 0, kvh * bs, id,
+                  policy);
+      tma_load_2d(scales + C::SCALES + j * 128, &vsmap, &my_bars[stage], kvh * bs * C::SB, id,
+                  policy);
+    }
+  };
+  if (lane == 0) {
+    for (int k = 0; k < min(R, my_count); ++k) issue(k);
+  }
+
+  MxState<QF, D> st;
+  const int64_t row0 = static_cast<int64_t>(s) * a.num_heads + kvh * group;
+  st.init(a, static_cast<const uint8_t*>(a.query) + row0 * D * 2, group, lane);
+  int k = 0;
+  for (; k < my_count; ++k) {
+    const int stage = k % R;
+    if (!__all_sync(FULL, mbar_wait(&my_bars[stage], (k / R) & 1, a.wait_limit_ns, &aborted)))
+      break;
+    const uint8_t* codes = my_codes + stage * C::STAGE;
+    const uint8_t* scales = my_scales + stage * C::SSTAGE;
+    st.template step<C::SWZ>(codes, codes + C::CODES, scales, scales + C::SCALES, half,
+                             min(kStep, tokens - (warp + k * NW) * kStep), lane);
+    __syncwarp();
+    if (lane == 0 && k + R < my_count) issue(k + R);
+  }
+  if (k < my_count) {
+    // a wait gave up (never expected): record it, let this warp's loads in
+    // flight land (bounded again), and stop the CTA after the barrier
+    if (lane == 0) {
+      record_failure(a.diag, kSiteTile, blockIdx.x, blockIdx.y, blockIdx.z, warp, k, my_count, 0);
+      aborted = 1;
+    }
+    for (int kk = k; kk < min(k + R, my_count); ++kk)
+      mbar_wait(&my_bars[kk % R], (kk / R) & 1, a.wait_limit_ns);
+  }
+
+  // merge the warps through shared memory (every issued load has landed)
+  __syncthreads();
+  const bool single = parts == 1;
+  if (aborted) {
+    // the unit's result is lost: zeros, or an empty partial that the combine
+    // kernel gives no weight, never stale data
+    if (threadIdx.x == 0) report(a.err, kErrWaitTimeout);
+    for (int idx = threadIdx.x; idx < group * D; idx += NW * 32) {
+      const int h = idx / D, d = idx % D;
+      if (single) {
+        store_out(QF{}, a.out, (row0 + h) * D + d, 0.f);
+      } else if (d == 0) {
+        a.ws_ml[(row0 + h) * a.max_parts + part] = make_float2(-CUDART_INF_F, 0.f);
+      }
+    }
+    return;
+  }
+  float* mbuf = reinterpret_cast<float*>(smem);  // [NW][8][2]: m, l
+  float* obuf = mbuf + NW * 16;                  // [NW][8][D]
+  st.finish(mbuf + warp * 16, obuf + warp * 8 * D, group, lane);
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < group * D; idx += NW * 32) {
+    const int h = idx / D, d = idx % D;
+    float M = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, mbuf[w * 16 + 2 * h]);
+    float L = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float mw = mbuf[w * 16 + 2 * h], lw = mbuf[w * 16 + 2 * h + 1];
+      // a warp that saw no token has m = -inf and l = 0; one that saw only
+      // NaN logits has m = -inf and l = NaN, which must survive
+      const float f = mw == -CUDART_INF_F ? (lw == 0.f ? 0.f : 1.f) : exp2f(mw - M);
+      L += lw * f;
+      o += obuf[(w * 8 + h) * D + d] * f;
+    }
+    o = L == 0.f ? 0.f : o / L;
+    if (single) {
+      store_out(QF{}, a.out, (row0 + h) * D + d, o);
+    } else {
+      const int64_t pi = (row0 + h) * a.max_parts + part;
+      a.ws_o[pi * D + d] = o;
+      // the combine kernel leaves out a partial whose sum is not positive: one
+      // that is NaN (o is NaN then) goes in with a weight of its own
+      if (d == 0) a.ws_ml[pi] = L == L ? make_float2(M, L) : make_float2(0.f, 1.f);
+    }
+  }
+}
+
+template <class QF, int D, int NW>
+cudaError_t launch_mx(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t stream) {
+  using C = MxCfg<D, NW>;
+  if (a.partition_blocks > kMaxUnitBlocks || kStep % a.block_size != 0)
+    return cudaErrorNotSupported;
+  const size_t smem = 1024 + C::OFF_IDS + 4 * static_cast<size_t>(a.partition_blocks);
+  auto kern = paged_decode_mxfp4_kernel<QF, D, NW>;
+  cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.num_kv_heads, a.num_seqs, a.max_parts), NW * 32, smem, stream, a,
+                    maps[0], maps[1], maps[2], maps[3]);
+}
+
+}  // namespace
+
+cudaError_t decode_mxfp4(const DecodeArgs& a, const CUtensorMap (&maps)[4], int q_dtype,
+                         int head_dim, cudaStream_t stream) {
+  if (q_dtype == kF16 && head_dim == 64) return launch_mx<F16, 64, 4>(a, maps, stream);
+  if (q_dtype == kF16 && head_dim == 128) return launch_mx<F16, 128, 4>(a, maps, stream);
+  if (q_dtype == kBF16 && head_dim == 64) return launch_mx<BF16, 64, 4>(a, maps, stream);
+  if (q_dtype == kBF16 && head_dim == 128) return launch_mx<BF16, 128, 4>(a, maps, stream);
+  return cudaErrorNotSupported;
+}
+
+}  // namespace paged
