@@ -768,7 +768,9 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     float m_used = -CUDART_INF_F, l = 0.f;
     bool ok = true;
     for (int k = 0; ok && k < nsteps; ++k) {
-      ok = mbar_wait(&s_bar[g][k & 1], (k >> 1) & 1, lim, &aborted);
+      // (whole warps go on or stop: the tensor-memory accesses below are
+      // executed by all lanes of a warp together)
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_bar[g][k & 1], (k >> 1) & 1, lim, &aborted));
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t t_s = t_grp + (SB == 2 ? (k & 1) * NT : 0) + lane_base;
@@ -934,10 +936,12 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // O is rescaled (rare: the maximum moves lazily) after P is written, when
       // fewer registers are live, and before P is posted; only once O += P V
       // of step k-1 completed. With one S buffer it has: S of this step was
-      // issued after it.
-      if (k >= 1 && rescale) {
+      // issued after it. A warp rescales when one of its rows does (alpha is
+      // 1 for the others): tensor-memory accesses take all of its lanes.
+      if (k >= 1 && __any_sync(0xffffffffu, rescale)) {
         if constexpr (SB == 2) {
-          ok = mbar_wait(&pv_bar[g][(k - 1) & 1], ((k - 1) >> 1) & 1, lim, &aborted);
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_bar[g][(k - 1) & 1], ((k - 1) >> 1) & 1,
+                                                 lim, &aborted));
           if (!ok) break;
           tc::fence_after_sync();
         }
@@ -957,7 +961,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       const int vrows = max(0, min(NT, kv_valid - tk0));
       if (!MX && vrows < NT) {  // (the converter warps wrote zeros there)
         uint8_t* vs = sv(k);
-        ok = mbar_wait(&vfull[k % VR], (k / VR) & 1, lim, &aborted);  // the TMA writes come first
+        // the TMA writes come first
+        ok = __all_sync(0xffffffffu, mbar_wait(&vfull[k % VR], (k / VR) & 1, lim, &aborted));
         if (!ok) break;
         for (int i = rr; i < (NT - vrows) * NSEG * 8; i += kTcRows) {
           const int r = vrows + i / (NSEG * 8), sg = (i / 8) % NSEG, c = i % 8;
@@ -971,7 +976,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       if (lane == 0) mbar_arrive(&p_bar[g][k & 1]);
     }
     if (ok)
-      ok = mbar_wait(&pv_bar[g][(nsteps - 1) & 1], ((nsteps - 1) >> 1) & 1, lim, &aborted);
+      ok = __all_sync(0xffffffffu, mbar_wait(&pv_bar[g][(nsteps - 1) & 1],
+                                             ((nsteps - 1) >> 1) & 1, lim, &aborted));
     // two copies of a row: the upper copy hands (maximum, sum, O) to the lower
     // through shared memory (Q's space, whose last reader, the last S, has
     // completed), column-major so that a warp's accesses are conflict-free;

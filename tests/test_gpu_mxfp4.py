@@ -356,6 +356,28 @@ def test_chunks_many_short_units():
     mx.check(out, ref, bound, "short units")
 
 
+@pytest.mark.parametrize("Hkv,group,D,dtype,n,qlen", [
+    (2, 8, 128, "bf16", 80, 8), (1, 1, 128, "f16", 3, 100), (1, 2, 64, "bf16", 2, 200)])
+def test_chunks_whose_rows_maxima_grow_apart(Hkv, group, D, dtype, n, qlen):
+    """Keys that grow along the context with a few large channels: the running maxima of a
+    warp's rows move at different steps."""
+    rng = np.random.default_rng(27)
+    ctxs = [int(c) for c in rng.integers(500, 700, n)]
+
+    def k_rows(shape):
+        return (rng.standard_normal(shape) * (1 + 3 * (rng.random(D) < 0.06)) *
+                np.exp2(rng.uniform(-2, 2, shape[:1] + (1, 1, 1))))
+    cache = mx.Cache(ctxs, Hkv, D, 16, rng, k_rows=k_rows)
+    q, qx = mx.query(rng, n * qlen, Hkv * group, D, dtype, amp=2.0)
+    scale = 1 / math.sqrt(D)
+    out, _ = run_chunk(q, cache, [qlen] * n, scale)
+    ref, bound = mx.attention(qx, cache, [qlen] * n, scale, dtype)
+    # a logit is a sum of |q||k| scale < 2^10 in all, off by 2^-22 of that: weights by a factor
+    # of 1 +- 2^-12, the output by 2^-11 of the largest value
+    top = np.abs(mx.values(cache.vc, np.where(cache.vs == 255, 0, cache.vs))).max()
+    mx.check(out, ref, bound + 2.0 ** -11 * top, "growing maxima")
+
+
 def test_chunks_bf16_full_range():
     """A bf16 query takes every scale the format has."""
     rng = np.random.default_rng(23)
