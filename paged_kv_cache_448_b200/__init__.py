@@ -235,63 +235,114 @@ def copy_blocks(src_key_cache, src_value_cache, dst_key_cache, dst_value_cache, 
 
 # ---------------------------------------------------------------- 4-bit cache
 
-def _call(fn, at, stream, *args) -> None:
-    """fn(*args, stream handle) with the device of tensor `at` current; without
-    a stream, that device's current one."""
-    import torch
-    if not at.is_cuda:
+# The calls below check what they are given in full and launch small kernels: the checks are
+# plain comparisons, and messages are put together only where one fails.
+
+class _Torch:
+    """What the checks use of torch, looked up once (torch is imported by whoever has tensors)."""
+
+    def __getattr__(self, name):
+        import torch
+        self.torch = torch
+        self.code = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+        self.int32, self.uint8 = torch.int32, torch.uint8
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        return self.__dict__[name]
+
+
+_t = _Torch()
+
+
+def _launch(fn, dev, stream, *args) -> None:
+    """fn(*args, stream handle) with CUDA device `dev` current; without a stream, that
+    device's current one."""
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if at.device.index == torch.cuda.current_device():
-        check(fn(*args, _stream_handle(stream)))
+    handle = _t.raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == _t.current_device():
+        status = fn(*args, handle)
     else:
-        with torch.cuda.device(at.device):
-            check(fn(*args, _stream_handle(stream)))
+        with _t.torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status:
+        check(status)
 
 
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _explain(tensors) -> None:
+    """Raise for the first of (name, tensor, dtypes, shape, device) that is not as it should
+    be; a None in a shape stands for any extent."""
+    for name, t, dtypes, shape, dev in tensors:
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+        if t.dim() != len(shape) or any(w not in (None, n) for w, n in zip(shape, t.shape)):
+            raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on another device ({t.device})")
 
 
-def _same_device(at, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != at.device:
-            raise ValueError(f"tensors on different devices ({at.device} and {t.device})")
-
-
-def _row_tensor(t, name: str) -> None:
-    _need(dtype_code(t) in (PA_F16, PA_BF16) and t.dim() == 3 and t.is_contiguous(),
-          f"{name} must be a contiguous f16 or bf16 [tokens, heads, head_dim] tensor")
-
-
-def _int_tensor(t, shape, name: str) -> None:
-    import torch
-    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-
-
-def _table_tensor(t, rows, name: str) -> None:
-    import torch
-    _need(t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous() and
-          rows in (None, t.shape[0]),
-          f"{name} must be a contiguous int32 [{'rows' if rows is None else rows}, "
-          "max_blocks_per_seq] tensor")
-
-
-def _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, head_dim):
+def _check_mxfp4_planes(kc, vc, ks, vs, D, dev):
     """(num_blocks, num_kv_heads, block_size) of an MXFP4 cache's planes."""
-    import torch
-    _need(key_cache.dim() == 4, "key_cache must be [num_blocks, num_kv_heads, block_size, "
-                                "head_dim / 2]")
-    NB, Hkv, BS = key_cache.shape[:3]
-    for t, width, name in ((key_cache, head_dim // 2, "key_cache"),
-                           (value_cache, head_dim // 2, "value_cache"),
-                           (k_scales, head_dim // 32, "k_scales"),
-                           (v_scales, head_dim // 32, "v_scales")):
-        _need(t.dtype == torch.uint8 and t.is_contiguous() and
-              tuple(t.shape) == (NB, Hkv, BS, width),
-              f"{name} must be a contiguous uint8 tensor of shape {[NB, Hkv, BS, width]}")
+    shape = kc.shape
+    if len(shape) != 4:
+        raise ValueError("key_cache must be [num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    NB, Hkv, BS, _ = shape
+    u8 = _t.uint8
+    codes, scales = (NB, Hkv, BS, D // 2), (NB, Hkv, BS, D // 32)
+    if not (shape == codes and vc.shape == codes and ks.shape == scales and
+            vs.shape == scales and kc.dtype is u8 and vc.dtype is u8 and ks.dtype is u8 and
+            vs.dtype is u8 and kc.is_contiguous() and vc.is_contiguous() and
+            ks.is_contiguous() and vs.is_contiguous() and kc.get_device() == dev and
+            vc.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev):
+        _explain([("key_cache", kc, (u8,), codes, dev), ("value_cache", vc, (u8,), codes, dev),
+                  ("k_scales", ks, (u8,), scales, dev), ("v_scales", vs, (u8,), scales, dev)])
     return NB, Hkv, BS
+
+
+def _check_pair(x, y, xname, yname):
+    """(pa_dtype, shape, device) of two 16-bit tensors [tokens, heads, head_dim] alike."""
+    shape, dt = x.shape, x.dtype
+    code, dev = _t.code.get(dt), x.get_device()
+    if not (code is not None and len(shape) == 3 and y.shape == shape and y.dtype is dt and
+            x.is_contiguous() and y.is_contiguous() and y.get_device() == dev):
+        _explain([(xname, x, tuple(_t.code), (None, None, None), dev),
+                  (yname, y, (dt,), tuple(shape), dev)])
+    return code, shape, dev
+
+
+def _check_ints(name, t, shape, dev):
+    if not (t.dtype is _t.int32 and t.shape == shape and t.is_contiguous() and
+            t.get_device() == dev):
+        _explain([(name, t, (_t.int32,), shape, dev)])
+
+
+def _check_table(name, t, rows, dev):
+    """(rows, max_blocks_per_seq) of a block table; rows None: any."""
+    shape = t.shape
+    if not (t.dtype is _t.int32 and len(shape) == 2 and rows in (None, shape[0]) and
+            t.is_contiguous() and t.get_device() == dev):
+        _explain([(name, t, (_t.int32,), (rows, None), dev)])
+    return shape
+
+
+def _check_workspace(t, dev):
+    if not (t.dtype is _t.uint8 and t.is_contiguous() and t.get_device() == dev):
+        _explain([("workspace", t, (_t.uint8,), (None,) * t.dim(), dev)])
+    return t.data_ptr(), t.numel()
+
+
+def _own_workspace(make, dev, stream):
+    """A workspace of one call's own, kept from reuse until `stream` has passed it."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    with _t.torch.cuda.device(dev):
+        ws = make()
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 def mxfp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
@@ -304,22 +355,23 @@ def mxfp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
                  for w in (head_dim // 2, head_dim // 2, head_dim // 32, head_dim // 32))
 
 
+def _mxfp4_rows(fn, key, value, kc, vc, ks, vs, slots, stream):
+    code, (T, Hkv, D), dev = _check_pair(key, value, "key", "value")
+    NB, heads, BS = _check_mxfp4_planes(kc, vc, ks, vs, D, dev)
+    if heads != Hkv:
+        raise ValueError(f"the cache has {heads} kv-heads, key {Hkv}")
+    _check_ints("slot_mapping", slots, (T,), dev)
+    _launch(fn, dev, stream, key.data_ptr(), value.data_ptr(), kc.data_ptr(), vc.data_ptr(),
+            ks.data_ptr(), vs.data_ptr(), slots.data_ptr(), T, Hkv, D, BS, NB, code)
+
+
 def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales,
                             slot_mapping, *, stream=None) -> None:
     """reshape_and_cache into an MXFP4 cache (pa_reshape_and_cache_mxfp4): key/value
     [T, Hkv, D] f16|bf16, planes as mxfp4_cache makes them, slot_mapping int32 [T]
     (negative = skip)."""
-    _row_tensor(key, "key")
-    _need(value.shape == key.shape and value.dtype == key.dtype and value.is_contiguous(),
-          "value must be contiguous, of key's shape and dtype")
-    T, Hkv, D = key.shape
-    NB, heads, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
-    _need(heads == Hkv, f"the cache has {heads} kv-heads, key {Hkv}")
-    _int_tensor(slot_mapping, (T,), "slot_mapping")
-    _same_device(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping)
-    _call(_native.lib().pa_reshape_and_cache_mxfp4, key, stream, _ptr(key), _ptr(value),
-          _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
-          _ptr(slot_mapping), T, Hkv, D, BS, NB, dtype_code(key))
+    _mxfp4_rows(_native.lib().pa_reshape_and_cache_mxfp4, key, value, key_cache, value_cache,
+                k_scales, v_scales, slot_mapping, stream)
 
 
 def gather_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, *,
@@ -327,33 +379,8 @@ def gather_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales, s
     """Rows of an MXFP4 cache by slot into key/value [T, Hkv, D] f16|bf16
     (pa_gather_cache_mxfp4); rows whose slot is negative or outside the pool stay
     as they were."""
-    _row_tensor(key, "key")
-    _need(value.shape == key.shape and value.dtype == key.dtype and value.is_contiguous(),
-          "value must be contiguous, of key's shape and dtype")
-    T, Hkv, D = key.shape
-    NB, heads, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
-    _need(heads == Hkv, f"the cache has {heads} kv-heads, key {Hkv}")
-    _int_tensor(slot_mapping, (T,), "slot_mapping")
-    _same_device(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping)
-    _call(_native.lib().pa_gather_cache_mxfp4, key, stream, _ptr(key), _ptr(value),
-          _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
-          _ptr(slot_mapping), T, Hkv, D, BS, NB, dtype_code(key))
-
-
-def _workspace_for(at, stream, make):
-    """A workspace of the call's own on `at`'s device, kept alive for `stream`."""
-    import torch
-    with torch.cuda.device(at.device):
-        ws = make()
-        if stream is not None:
-            ws.record_stream(stream)
-    return ws
-
-
-def _check_workspace(ws) -> None:
-    import torch
-    _need(ws.dtype == torch.uint8 and ws.is_contiguous(), "workspace must be a contiguous uint8 "
-                                                          "tensor")
+    _mxfp4_rows(_native.lib().pa_gather_cache_mxfp4, key, value, key_cache, value_cache,
+                k_scales, v_scales, slot_mapping, stream)
 
 
 def decode_mxfp4(out, query, key_cache, value_cache, k_scales, v_scales, block_tables,
@@ -362,25 +389,20 @@ def decode_mxfp4(out, query, key_cache, value_cache, k_scales, v_scales, block_t
     """decode over an MXFP4 cache (pa_decode_mxfp4): out/query [S, H, D] f16|bf16, planes as
     mxfp4_cache makes them; workspace from decode_workspace(..., cache_dtype=PA_MXFP4).
     Returns ``out``."""
-    _row_tensor(query, "query")
-    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
-          "out must be contiguous, of query's shape and dtype")
-    S, H, D = query.shape
-    NB, Hkv, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
-    _table_tensor(block_tables, S, "block_tables")
-    _int_tensor(context_lens, (S,), "context_lens")
+    code, (S, H, D), dev = _check_pair(query, out, "query", "out")
+    NB, Hkv, BS = _check_mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D, dev)
+    _, width = _check_table("block_tables", block_tables, S, dev)
+    _check_ints("context_lens", context_lens, (S,), dev)
     if workspace is None:
-        workspace = _workspace_for(query, stream, lambda: decode_workspace(
-            S, H, Hkv, D, BS, max_context_len, partition_tokens, device=query.device,
-            stream=stream, cache_dtype=PA_MXFP4))
-    _check_workspace(workspace)
-    _same_device(query, out, key_cache, value_cache, k_scales, v_scales, block_tables,
-                 context_lens, workspace)
-    _call(_native.lib().pa_decode_mxfp4, query, stream, _ptr(out), _ptr(query), _ptr(key_cache),
-          _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), int(max_context_len), S, H, Hkv, D, BS, NB,
-          float(scale), dtype_code(query), int(partition_tokens), _ptr(workspace),
-          workspace.numel())
+        workspace = _own_workspace(lambda: decode_workspace(
+            S, H, Hkv, D, BS, max_context_len, partition_tokens, stream=stream,
+            cache_dtype=PA_MXFP4), dev, stream)
+    ws, ws_bytes = _check_workspace(workspace, dev)
+    _launch(_native.lib().pa_decode_mxfp4, dev, stream, out.data_ptr(), query.data_ptr(),
+            key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
+            int(max_context_len), S, H, Hkv, D, BS, NB, float(scale), code,
+            int(partition_tokens), ws, ws_bytes)
     return out
 
 
@@ -390,27 +412,21 @@ def chunked_prefill_mxfp4(out, query, cu_query_lens, max_query_len: int, key_cac
     """chunked_prefill over an MXFP4 cache (pa_chunked_prefill_mxfp4): out/query [T, H, D]
     f16|bf16, planes as mxfp4_cache makes them; workspace from
     chunked_prefill_workspace(..., PA_MXFP4). Returns ``out``."""
-    _row_tensor(query, "query")
-    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
-          "out must be contiguous, of query's shape and dtype")
-    T, H, D = query.shape
-    S = context_lens.shape[0]
-    NB, Hkv, BS = _mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D)
-    _table_tensor(block_tables, S, "block_tables")
-    _int_tensor(context_lens, (S,), "context_lens")
-    _int_tensor(cu_query_lens, (S + 1,), "cu_query_lens")
+    code, (T, H, D), dev = _check_pair(query, out, "query", "out")
+    NB, Hkv, BS = _check_mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D, dev)
+    S, width = _check_table("block_tables", block_tables, None, dev)
+    _check_ints("context_lens", context_lens, (S,), dev)
+    _check_ints("cu_query_lens", cu_query_lens, (S + 1,), dev)
     if workspace is None:
-        workspace = _workspace_for(query, stream, lambda: chunked_prefill_workspace(
-            S, T, H, Hkv, D, max_query_len, max_context_len, PA_MXFP4, device=query.device,
-            stream=stream))
-    _check_workspace(workspace)
-    _same_device(query, out, key_cache, value_cache, k_scales, v_scales, block_tables,
-                 context_lens, cu_query_lens, workspace)
-    _call(_native.lib().pa_chunked_prefill_mxfp4, query, stream, _ptr(out), _ptr(query),
-          _ptr(cu_query_lens), T, int(max_query_len), _ptr(key_cache), _ptr(value_cache),
-          _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
-          _ptr(context_lens), int(max_context_len), S, H, Hkv, D, BS, NB, float(scale),
-          dtype_code(query), _ptr(workspace), workspace.numel())
+        workspace = _own_workspace(lambda: chunked_prefill_workspace(
+            S, T, H, Hkv, D, max_query_len, max_context_len, PA_MXFP4, stream=stream), dev,
+            stream)
+    ws, ws_bytes = _check_workspace(workspace, dev)
+    _launch(_native.lib().pa_chunked_prefill_mxfp4, dev, stream, out.data_ptr(),
+            query.data_ptr(), cu_query_lens.data_ptr(), T, int(max_query_len),
+            key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
+            int(max_context_len), S, H, Hkv, D, BS, NB, float(scale), code, ws, ws_bytes)
     return out
 
 
@@ -426,19 +442,27 @@ class CachePool:
 
     def __init__(self, planes, block_size: int):
         planes = list(planes)
-        _need(len(planes) > 0, "a pool has at least one plane")
+        if not planes:
+            raise ValueError("a pool has at least one plane")
         first = planes[0]
         for t in planes:
-            _need(t.dim() >= 2 and t.is_contiguous() and t.shape[0] == first.shape[0] and
-                  t.shape[0] > 0,
-                  "planes must be contiguous [num_blocks, ...] tensors of as many blocks")
-        _need(first.is_cuda, "planes must be on a CUDA device")
-        _same_device(first, *planes)
+            if not (t.dim() >= 2 and t.is_contiguous() and t.shape[0] == first.shape[0] > 0):
+                raise ValueError("planes must be contiguous [num_blocks, ...] tensors of as "
+                                 "many blocks")
+            if not t.is_cuda or t.device != first.device:
+                raise ValueError("planes must be on one CUDA device")
         self.planes = planes
         self.block_size = int(block_size)
         self.num_blocks = int(first.shape[0])
+        self._dev = first.get_device()
         self._array = (_native.Plane * len(planes))(
-            *[_native.Plane(t.data_ptr(), t[0].numel() * t.element_size()) for t in planes])
+            *[_native.Plane(t.data_ptr(), t.stride(0) * t.element_size()) for t in planes])
+
+    def _word(self, error_word):
+        if error_word is None:
+            return None
+        _check_ints("error_word", error_word, (1,), self._dev)
+        return error_word.data_ptr()
 
     def fork(self, block_tables, context_lens, parents, fresh_blocks, new_block_tables,
              new_context_lens, *, error_word=None, stream=None) -> None:
@@ -446,37 +470,32 @@ class CachePool:
         parent's whole blocks; a last block that is not full is copied into block
         fresh_blocks[i] of every plane (a negative entry shares it). Writes
         new_block_tables int32 [n, max_blocks_per_seq] and new_context_lens int32 [n]."""
-        _table_tensor(block_tables, None, "block_tables")
-        S, width = block_tables.shape
-        _int_tensor(context_lens, (S,), "context_lens")
-        n = parents.shape[0] if parents.dim() == 1 else -1
-        _int_tensor(parents, (n,), "parents")
-        _int_tensor(fresh_blocks, (n,), "fresh_blocks")
-        _int_tensor(new_block_tables, (n, width), "new_block_tables")
-        _int_tensor(new_context_lens, (n,), "new_context_lens")
-        if error_word is not None:
-            _int_tensor(error_word, (1,), "error_word")
-        _same_device(self.planes[0], block_tables, context_lens, parents, fresh_blocks,
-                     new_block_tables, new_context_lens, error_word)
-        _call(_native.lib().pa_fork_sequences, self.planes[0], stream, self._array,
-              len(self.planes), self.num_blocks, self.block_size, _ptr(block_tables), S, width,
-              _ptr(context_lens), _ptr(parents), _ptr(fresh_blocks), n, _ptr(new_block_tables),
-              _ptr(new_context_lens), _ptr(error_word))
+        dev = self._dev
+        S, width = _check_table("block_tables", block_tables, None, dev)
+        n = parents.numel()
+        _check_ints("context_lens", context_lens, (S,), dev)
+        _check_ints("parents", parents, (n,), dev)
+        _check_ints("fresh_blocks", fresh_blocks, (n,), dev)
+        _check_ints("new_block_tables", new_block_tables, (n, width), dev)
+        _check_ints("new_context_lens", new_context_lens, (n,), dev)
+        _launch(_native.lib().pa_fork_sequences, dev, stream, self._array, len(self.planes),
+                self.num_blocks, self.block_size, block_tables.data_ptr(), S, width,
+                context_lens.data_ptr(), parents.data_ptr(), fresh_blocks.data_ptr(), n,
+                new_block_tables.data_ptr(), new_context_lens.data_ptr(),
+                self._word(error_word))
 
     def compact(self, moves, block_tables=None, *, error_word=None, stream=None) -> None:
         """Move blocks moves[i, 0] -> moves[i, 1] in every plane and rename them in
         block_tables, in place (pa_compact_blocks; BlockAllocator.compact makes the list)."""
-        _need(moves.dim() == 2, "moves must be a contiguous int32 [n, 2] tensor")
-        _int_tensor(moves, (moves.shape[0], 2), "moves")
+        dev = self._dev
+        n = moves.shape[0] if moves.dim() else 0
+        _check_ints("moves", moves, (n, 2), dev)
+        table, entries = None, 0
         if block_tables is not None:
-            _table_tensor(block_tables, None, "block_tables")
-        if error_word is not None:
-            _int_tensor(error_word, (1,), "error_word")
-        _same_device(self.planes[0], moves, block_tables, error_word)
-        _call(_native.lib().pa_compact_blocks, self.planes[0], stream, self._array,
-              len(self.planes), self.num_blocks, _ptr(moves), moves.shape[0],
-              _ptr(block_tables), 0 if block_tables is None else block_tables.numel(),
-              _ptr(error_word))
+            _check_table("block_tables", block_tables, None, dev)
+            table, entries = block_tables.data_ptr(), block_tables.numel()
+        _launch(_native.lib().pa_compact_blocks, dev, stream, self._array, len(self.planes),
+                self.num_blocks, moves.data_ptr(), n, table, entries, self._word(error_word))
 
 
 def sha256(data: bytes) -> bytes:

@@ -92,6 +92,12 @@ class PagedError(RuntimeError):
 
 def lib() -> ctypes.CDLL:
     """The loaded libpaged.so (raises if it has not been built)."""
+    if _lib is not None:
+        return _lib
+    return _load()
+
+
+def _load() -> ctypes.CDLL:
     global _lib
     with _lock:
         if _lib is None:
