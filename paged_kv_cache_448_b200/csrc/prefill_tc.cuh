@@ -45,10 +45,14 @@
 // memory as an E4M3 hi part and an E5M2 residual, so O += P V takes two
 // 8-bit MMAs with V read MN-major; the V scale applies in the epilogue.
 // An MXFP4 cache (mxfp4.cuh) is widened to the query's type on its way into
-// shared memory: in place of the TMA warps, CW converter warps per ring load
-// codes and scales into registers two steps ahead, and once the MMAs that read
-// a stage completed they write code * 2^(b - 127) into it in the layout the
-// TMA boxes have. From there on it is the 16-bit kernel.
+// shared memory: in place of the TMA warps, seven converter warps load codes
+// and scales into registers, some items ahead (an item is 32 blocks of 32
+// codes: 8 rows of 128 dims), and once the MMAs that read a stage completed
+// they write code * 2^(b - 127) into it in the layout the TMA boxes have. From
+// there on it is the 16-bit kernel. The warps take the items of K and V in one
+// order, K a step ahead of V; a stage is full when each of its items arrived.
+// The register file is shared out anew once the roles are known (softmax
+// warps more, the others less).
 // Every wait is bounded by wall time. A wait that gives up sets a shared
 // abort flag that ends the other roles' waits; the MMA warp lets its issued
 // MMAs and the TMA warp its issued loads complete (bounded) before the
@@ -94,9 +98,17 @@ struct TcCfg {
   static constexpr bool FP8 = CF::kBytes == 1;
   static constexpr bool MX = std::is_same<CF, Mxfp4>::value;
   static constexpr bool BF = std::is_same<QF, BF16>::value;
-  // warps besides the softmax warps: MMA issue, then the loaders of K and of V
-  static constexpr int CW = MX ? (NG == 2 ? 2 : 1) : 1;  // loader warps per ring
-  static constexpr int THREADS = NG * kTcRows + 32 + 64 * CW;
+  // warps besides the softmax warps: MMA issue, then the loaders
+  static constexpr int CW = MX ? 7 : 2;
+  static constexpr int THREADS = NG * kTcRows + 32 + 32 * CW;
+  // MXFP4: registers per thread at launch (what __launch_bounds__ leaves), of
+  // the softmax warps and of the other eight; the same total before and after
+  static constexpr int LAUNCH_REGS = NG == 2 ? 128 : 80;
+  static constexpr int SOFTMAX_REGS = NG == 2 ? 168 : 128;
+  static constexpr int OTHER_REGS = NG == 2 ? 88 : 56;
+  static_assert(!MX || (NG * kTcRows * SOFTMAX_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS &&
+                        THREADS == NG * kTcRows + 256),
+                "register shares");
   static constexpr int NSEG = D * CF::kBytes / 128;  // 128-byte segments of a cache row
   static_assert(NSEG >= 1, "rows of at least 128 bytes");
   static constexpr int ROWS = NG * kTcRows;
@@ -205,19 +217,23 @@ struct TcCache<Mxfp4> {
 };
 
 // 32 codes of one block and their scale byte -> 32 values of the query's type
-// (rounded to nearest), four 16-byte chunks.
+// (rounded to nearest), four 16-byte chunks of 8 dims.
 //  * f16: a power of two 2^(b - 127) from 2^-24 to 2^13, so that no product
 //    overflows; below it 0, above it 2^13. Exact for caches written from f16
 //    rows, but for codes below f16's own resolution.
-//  * bf16: the E2M1 value's f16 bits moved into the bf16 fields stand for the
-//    value times 2^-112; the factor 2^(b - 15) undoes it (exact; scales above
-//    2^15 in two factors).
+//  * bf16: the code's three magnitude bits placed over the exponent's lowest
+//    two bits and the mantissa's highest are the value times 2^-126 (E2M1's
+//    subnormal 0.5 included); 2^100 and 2^(b - 101) undo it and apply the
+//    scale (exact; scales above 2^101 in a third factor). This takes half the
+//    integer instructions of converting to f16 first and moving the fields,
+//    and leaves the dims of a chunk in the order 0 4 1 5 2 6 3 7, which Q's
+//    chunks follow (permute_chunk) and the epilogue undoes for V (chunk_at).
 template <bool BF>
 __device__ __forceinline__ void mx_widen(const uint4& codes, int b, uint4 (&out)[4]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t f;
   if constexpr (BF) {
-    f = b == kMxNan ? 0x7fc0u : b == 0 ? 0u : static_cast<uint32_t>(min(b, 142) + 112) << 7;
+    f = b == kMxNan ? 0x7fc0u : b == 0 ? 0u : static_cast<uint32_t>(min(b + 26, 254)) << 7;
   } else {
     f = b == kMxNan ? 0x7e00u
         : b > 112   ? static_cast<uint32_t>(min(b, 140) - 112) << 10
@@ -227,27 +243,33 @@ __device__ __forceinline__ void mx_widen(const uint4& codes, int b, uint4 (&out)
   f *= 0x10001u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t h[4], o[4];
-    mx_unpack8(w[i], h);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (BF) {
-        const uint32_t t = ((h[j] >> 3) & 0x0fff0fffu) | (h[j] & 0x80008000u);
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&t),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&f));
-        o[j] = *reinterpret_cast<const uint32_t*>(&r);
-      } else {
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[j]),
-                                  *reinterpret_cast<const __half2*>(&f));
-        o[j] = *reinterpret_cast<const uint32_t*>(&r);
-      }
-    }
-    if (BF && b > 142 && b != kMxNan) {
-      const uint32_t f2 = (static_cast<uint32_t>(b - 142 + 127) << 7) * 0x10001u;
+    uint32_t o[4];
+    if constexpr (BF) {
+      auto mul = [](uint32_t x, uint32_t y) {
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&r);
+      };
+      // nibbles j and j + 4, one in each half: magnitude at bits 6-8, sign at 15
+      const uint32_t m[4] = {w[i] << 6, w[i] << 2, w[i] >> 2, w[i] >> 6};
+      const uint32_t sg[4] = {w[i] << 12, w[i] << 8, w[i] << 4, w[i]};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&f2));
+        const uint32_t t = (m[j] & 0x01c001c0u) | (sg[j] & 0x80008000u);
+        o[j] = mul(mul(t, 0x71807180u), f);  // 0x7180: 2^100
+      }
+      if (b > 228 && b != kMxNan) {
+        const uint32_t f2 = static_cast<uint32_t>((b - 228 + 127) << 7) * 0x10001u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = mul(o[j], f2);
+      }
+    } else {
+      uint32_t h[4];
+      mx_unpack8(w[i], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[j]),
+                                  *reinterpret_cast<const __half2*>(&f));
         o[j] = *reinterpret_cast<const uint32_t*>(&r);
       }
     }
@@ -255,18 +277,31 @@ __device__ __forceinline__ void mx_widen(const uint4& codes, int b, uint4 (&out)
   }
 }
 
-// Raw codes and scale bytes of one step in one thread of a converter warp:
-// item j of warp w covers rows (j CW + w) RPI .. of the step, one 32-element
-// block a lane.
-template <class C, int D>
+// A chunk of 8 16-bit values in the order mx_widen leaves bf16 values in.
+__device__ __forceinline__ uint4 permute_chunk(const uint4& v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+}
+
+// Column of dim d (0..7) within a chunk of 8: as stored, or in that order.
+template <bool PERMUTED>
+__host__ __device__ constexpr int chunk_at(int d) {
+  return PERMUTED ? (d < 4 ? 2 * d : 2 * (d - 4) + 1) : d;
+}
+
+// One converter lane's share of an item: 32 codes and their scale byte.
 struct MxRaw {
-  static constexpr int NB = D / 32;                        // blocks of a row
-  static constexpr int RPI = 32 / NB;                      // rows of an item
-  static constexpr int ITEMS = C::NT / (RPI * C::CW);
-  static_assert(16 % RPI == 0 && ITEMS * RPI * C::CW == C::NT, "items within blocks of the pool");
-  uint4 codes[ITEMS];
-  uint32_t scale[ITEMS];
+  uint4 codes;
+  uint32_t scale;
 };
+
+__device__ __forceinline__ void mx_load(MxRaw& raw, const uint8_t* codes, const uint8_t* scale) {
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(raw.codes.x), "=r"(raw.codes.y), "=r"(raw.codes.z), "=r"(raw.codes.w)
+               : "l"(codes)
+               : "memory");
+  asm volatile("ld.global.cg.u8 %0, [%1];" : "=r"(raw.scale) : "l"(scale) : "memory");
+}
 
 template <class QF, class CF, int D, int G, int NG>
 __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 : 1)
@@ -276,7 +311,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   constexpr int NSEG = C::NSEG, QT = C::QT, KR = C::KR, VR = C::VR, NT = C::NT, TR = kTileRows;
   constexpr int SB = C::SB, H = C::H;
   constexpr int kMma = NG * kTcRows / 32;   // warp issuing the MMAs (owns the tensor memory)
-  constexpr int kLoader = kMma + 1;         // loader warps: K's, then V's
+  constexpr int kLoader = kMma + 1;         // loader warps (TMA: K's, then V's)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -299,11 +334,11 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const uint64_t lim = a.wait_limit_ns;
   if (tid == 0) {
     for (int r = 0; r < KR; ++r) {
-      mbar_init(&kfull[r], MX ? C::CW : 1);
+      mbar_init(&kfull[r], MX ? NT / (1024 / D) : 1);
       mbar_init(&kempty[r], 1);
     }
     for (int r = 0; r < VR; ++r) {
-      mbar_init(&vfull[r], MX ? C::CW : 1);
+      mbar_init(&vfull[r], MX ? NT / (1024 / D) : 1);
       mbar_init(&vempty[r], 1);
     }
     for (int g = 0; g < NG; ++g)
@@ -396,7 +431,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       for (int sg = 0; sg < NSEG; ++sg)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
+          uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (MX && BF) v = permute_chunk(v);
           *reinterpret_cast<uint4*>(sq(g) + sg * C::QPART + sw128(rr, c)) = v;
         }
     } else {
@@ -445,91 +481,104 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  // whole warpgroups: the eight other warps here, the softmax warps in their branch
+  if constexpr (MX) {
+    if (warp >= kMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+  }
 
   if (MX && warp >= kLoader) {
     if constexpr (MX) {
-      // ================= converter warps: CW for K, CW for V =================
-      using Raw = MxRaw<C, D>;
-      constexpr int NB = Raw::NB, RPI = Raw::RPI, ITEMS = Raw::ITEMS, CW = C::CW;
-      const bool is_v = warp >= kLoader + CW;
-      const int w = (warp - kLoader) % CW;
-      const int R = is_v ? VR : KR;
-      uint64_t* full = is_v ? vfull : kfull;
-      uint64_t* empty = is_v ? vempty : kempty;
-      const uint8_t* codes = cache.codes[is_v];
-      const uint8_t* scales = cache.scales[is_v];
+      // ================= converter warps =================
+      constexpr int NB = D / 32, RPI = 32 / NB;  // blocks of a row, rows of an item
+      constexpr int ITEMS = NT / RPI;            // items of a stage
+      constexpr int AHEAD = 4;                   // items in flight per warp
+      static_assert(16 % RPI == 0 && (ITEMS & (ITEMS - 1)) == 0, "an item within one block");
       const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-      const int bs = a.block_size;
-      const int kv_end = min(ctx, tend * TR);  // tokens of this CTA's part
+      const int bs_log = a.block_size == 32 ? 5 : 4;
+      const int kv_end = min(ctx, tend * TR);  // end of this CTA's tokens
       // lane -> (row of the item, block): eight lanes that store together
       // write four rows x two blocks of one segment, in eight different
       // 16-byte columns of the swizzled tile
       const int lb = NB == 4 ? (lane >> 4) * 2 + (lane & 1) : (lane & 1);
       const int lr = NB == 4 ? (lane >> 1) & 7 : lane >> 1;
-      auto load_ids = [&](int k, int32_t (&id)[ITEMS]) {
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-          const int t = (kbase + k) * NT + (j * CW + w) * RPI;
-          id[j] = k < nsteps && t < kv_end ? table[t / bs] : 0;
-        }
+      // Item n of the CTA is item n % ITEMS of chunk c = n / ITEMS, the chunks
+      // in the order K0, K1 V0, K2 V1, ... (the K past the last step is empty).
+      auto is_v = [](uint32_t n) { return n >= 2 * ITEMS && ((n / ITEMS) & 1) == 0; };
+      auto step_of = [&](uint32_t n) {
+        const int c = static_cast<int>(n / ITEMS);
+        return is_v(n) ? c / 2 - 1 : (c + 1) / 2;
       };
-      auto load = [&](int k, const int32_t (&id)[ITEMS], Raw& raw) {
-        if (k >= nsteps) return;
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-          const int t = (kbase + k) * NT + (j * CW + w) * RPI + lr;
-          raw.codes[j] = make_uint4(0u, 0u, 0u, 0u);
-          raw.scale[j] = 0u;
-          if (t < kv_end && id[j] >= 0 && id[j] < a.num_blocks) {
-            const int64_t row =
-                (static_cast<int64_t>(id[j]) * a.num_kv_heads + kvh) * bs + t % bs;
-            raw.codes[j] = __ldcg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + lb);
-            raw.scale[j] = __ldcg(scales + row * NB + lb);
-          } else if (t < kv_end && !is_v && lane == 0) {
-            report(a.err, kErrBadBlockId);  // the block reads as zeros
-          }
-        }
+      const uint32_t total = (2 * nsteps + 1) * ITEMS;
+      auto token = [&](uint32_t n) {
+        return (kbase + step_of(n)) * NT + static_cast<int>(n % ITEMS) * RPI;
+      };
+      // block id of item n, INT32_MAX where it has no tokens
+      auto load_id = [&](uint32_t n) {
+        const int t = token(n);
+        if (n >= total || t >= kv_end) return INT32_MAX;
+        const int32_t b = __ldg(table + (t >> bs_log));
+        return b;
+      };
+      // loads of item n, whose block is id; a row that is not there reads block 0
+      // and is given the scale byte 0 when it is used
+      auto load = [&](uint32_t n, int32_t id, MxRaw& raw) {
+        const int t = token(n) + lr;
+        const bool there = id >= 0 && id < a.num_blocks && t < kv_end && n < total;
+        if (!there && lane == 0 && n < total && t < kv_end) report(a.err, kErrBadBlockId);
+        const int64_t row =
+            ((there ? static_cast<int64_t>(id) : 0) * a.num_kv_heads + kvh) * a.block_size +
+            (t & (a.block_size - 1));
+        const int v = is_v(n);
+        mx_load(raw, cache.codes[v] + row * (D / 2) + lb * 16, cache.scales[v] + row * NB + lb);
+        return there;
       };
       bool ok = true;
-      auto step = [&](int k, Raw& raw) {
+      auto convert = [&](uint32_t n, const MxRaw& raw, bool there) {
+        const int k = step_of(n), j = static_cast<int>(n % ITEMS);
+        if (k >= nsteps) return;  // (the K past the last step)
+        const bool v = is_v(n);
+        const int R = v ? VR : KR;
         if (k >= R)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&empty[k % R], ((k - R) / R) & 1, lim, &aborted));
+          ok = __all_sync(0xffffffffu, mbar_wait(v ? &vempty[k % VR] : &kempty[k % KR],
+                                                 ((k - R) / R) & 1, lim, &aborted));
         if (!ok) return;
         const int t_begin = (kbase + k) * (NT / TR), t_end = min(tend, t_begin + NT / TR);
-        if (!is_v && a.skip_tile >= t_begin - tbase && a.skip_tile < t_end - tbase &&
+        if (!v && a.skip_tile >= t_begin - tbase && a.skip_tile < t_end - tbase &&
             skip_unit_for_test(a.skip_tile, a.skip_tile, first_unit))
-          return;  // (the step is never posted)
-        uint8_t* stage = is_v ? sv(k) : sk(k);
+          return;  // (the step is never complete)
+        uint4 o[4];
+        mx_widen<BF>(raw.codes, there ? static_cast<int>(raw.scale) : 0, o);
+        const int r = j * RPI + lr;
+        uint8_t* seg = (v ? sv(k) : sk(k)) + (lb / 2) * C::KV_SEG;
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-          uint4 o[4];
-          mx_widen<BF>(raw.codes[j], static_cast<int>(raw.scale[j]), o);
-          const int r = (j * CW + w) * RPI + lr;
-          uint8_t* seg = stage + (lb / 2) * C::KV_SEG;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(seg + sw128(r, (lb & 1) * 4 + i)) = o[i];
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(seg + sw128(r, (lb & 1) * 4 + i)) = o[i];
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[k % R]);
+        if (lane == 0) mbar_arrive(v ? &vfull[k % VR] : &kfull[k % KR]);
       };
-      Raw r0, r1;
-      int32_t id[ITEMS];
-      load_ids(0, id);
-      load(0, id, r0);
-      load_ids(1, id);
-      load(1, id, r1);
-      load_ids(2, id);
-      for (int k = 0; ok && k < nsteps; k += 2) {
-        step(k, r0);
-        load(k + 2, id, r0);
-        load_ids(k + 3, id);
-        if (!ok || k + 1 >= nsteps) break;
-        step(k + 1, r1);
-        load(k + 3, id, r1);
-        load_ids(k + 4, id);
+      // this warp's items are w, w + CW, ...; slot i of the rotating registers
+      // holds the loads of item n + i CW, and the block id of item n + (i + AHEAD) CW
+      MxRaw raw[AHEAD];
+      bool there[AHEAD];
+      int32_t id[AHEAD];
+      uint32_t n = warp - kLoader;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) id[i] = load_id(n + i * C::CW);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        there[i] = load(n + i * C::CW, id[i], raw[i]);
+        id[i] = load_id(n + (i + AHEAD) * C::CW);
+      }
+      for (; ok && n < total; n += AHEAD * C::CW) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const uint32_t m = n + i * C::CW;
+          if (!ok || m >= total) break;
+          convert(m, raw[i], there[i]);
+          there[i] = load(m + AHEAD * C::CW, id[i], raw[i]);
+          id[i] = load_id(m + 2 * AHEAD * C::CW);
+        }
       }
       if (!ok && lane == 0) {
         aborted = 1;
@@ -758,6 +807,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     __syncwarp();  // whole warps reach the CTA barrier below
   } else {
     // ================= softmax warps: one row per thread =================
+    if constexpr (MX) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     const int g = warp / 4;                      // row group
     const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t t_grp = tmem + g * kTmemGroup;
@@ -780,7 +830,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // group, or an E4M3 cache, 64 at a time (measured on B200 with the
       // fixed MMA order, chunked prefill: bf16 687 against 657 TFLOP/s held
       // and not; E4M3 733 against 781, its softmax needing more registers)
-      constexpr bool kHoldAll = NG == 2 && !FP8 && !MX;
+      constexpr bool kHoldAll = NG == 2 && !FP8;
       float x[kHoldAll ? 128 : 64];
       float mraw = -CUDART_INF_F;
       // this row's logits of 64-token half h, masked after the row's position
@@ -1036,6 +1086,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // a split key range, (max, sum) and O / l in fp32 for the combine
       // kernel (a row that sees none of the part's tokens leaves -inf, 0, 0)
       tc::fence_after_sync();
+      auto at = [](int d) { return d / 8 * 8 + chunk_at<MX && BF>(d % 8); };  // column of a dim
       const float inv = (l > 0.f ? 1.f / l : 0.f) * (FP8 ? a.v_scale[kvh] : 1.f);
       if (parts == 1) {
         uint4* o4 = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row_off * 2);
@@ -1050,10 +1101,10 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
           if (out_row) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              o4[c * 4 + q] = make_uint4(pack_pair(BF, o[8 * q] * inv, o[8 * q + 1] * inv),
-                                         pack_pair(BF, o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                         pack_pair(BF, o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                         pack_pair(BF, o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+              o4[c * 4 + q] = make_uint4(pack_pair(BF, o[at(8 * q)] * inv, o[at(8 * q + 1)] * inv),
+                                         pack_pair(BF, o[at(8 * q + 2)] * inv, o[at(8 * q + 3)] * inv),
+                                         pack_pair(BF, o[at(8 * q + 4)] * inv, o[at(8 * q + 5)] * inv),
+                                         pack_pair(BF, o[at(8 * q + 6)] * inv, o[at(8 * q + 7)] * inv));
           }
         }
       } else {
@@ -1071,8 +1122,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
           if (out_row) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              w4[c * 8 + q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv,
-                                          o[4 * q + 3] * inv);
+              w4[c * 8 + q] = make_float4(o[at(4 * q)] * inv, o[at(4 * q + 1)] * inv,
+                                          o[at(4 * q + 2)] * inv, o[at(4 * q + 3)] * inv);
           }
         }
       }
@@ -1098,6 +1149,15 @@ cudaError_t launch_tc(const PrefillArgs& a, const TcCache<CF>& cache, int32_t ma
   if (e != cudaSuccess) return e;
   if (a.q_tiles != (max_query_len + C::QT - 1) / C::QT) return cudaErrorInvalidValue;
   if (a.max_parts > 1 && a.partition_tiles % (C::NT / kTileRows) != 0) return cudaErrorInvalidValue;
+  if constexpr (C::MX) {
+    // the shares of the register file hold for the launch's total alone: with
+    // less the softmax warps would wait for registers that never come
+    static const int regs = [&] {
+      cudaFuncAttributes at{};
+      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < C::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
+  }
   PrefillArgs b = a;
   b.dup_rows = NG == 1 && static_cast<int64_t>(max_query_len) * G <= kTcRows / 2 ? 1 : 0;
   e = launch_pdl(kern, dim3(static_cast<unsigned>(a.q_tiles * a.max_parts), a.num_kv_heads,
