@@ -903,8 +903,9 @@ PA_API pa_status pa_chunked_prefill_mxfp4(
                 block_size);
   if (q_dtype != PA_F16 && q_dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: query must be f16 or bf16");
-  if (num_blocks > INT32_MAX)
-    return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: pool too large");
+  if (num_blocks > INT32_MAX ||
+      static_cast<int64_t>(num_kv_heads) * block_size * (head_dim / 2) > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "chunked_prefill_mxfp4: pool or block too large");
   if (num_seqs > 65535 || num_kv_heads > 65535)
     return fail(PA_ERR_UNSUPPORTED,
                 "chunked_prefill_mxfp4: more than 65535 sequences or kv-heads");

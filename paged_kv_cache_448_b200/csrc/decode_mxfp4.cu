@@ -119,6 +119,62 @@ __device__ __forceinline__ uint32_t f16_pow2(uint32_t x, int r) {
   return x * 0x400u + static_cast<uint32_t>(15 - r) * 0x04000400u;
 }
 
+// f16 of 2^(v - r) for the halves v of x with max(r - below, 1) <= v <= r + 7,
+// 0 for the others (a scale byte of 0 reads as 0).
+__device__ __forceinline__ uint32_t weights(uint32_t x, int r, int below) {
+  const int lo = max(r - below, 1);
+  const uint32_t in = halves_within(x, lo, r + 7);
+  const uint32_t keep = ((in & 0xffffu) ? 0x0000ffffu : 0u) | ((in >> 16) ? 0xffff0000u : 0u);
+  // the halves left out take the value r first: no carry into the other half
+  return f16_pow2(in | (static_cast<uint32_t>(max(r, 0)) * 0x10001u & ~keep), max(r, 0)) & keep;
+}
+
+// m's bits of x, the others of y.
+__device__ __forceinline__ uint32_t bit_select(uint32_t m, uint32_t x, uint32_t y) {
+  return ((x ^ y) & m) ^ y;
+}
+
+// One word of V codes as ldmatrix.trans gives it (dims 4 g .. + 3 of tokens
+// 2 c, 2 c + 1) -> per dim the f16 pair of the two tokens.
+__device__ __forceinline__ void v_pairs(uint32_t w, uint32_t (&h)[4]) {
+  // bytes: (token 2c, token 2c + 1) codes of dims 0, 2, 1, 3
+  const uint32_t x =
+      bit_select(0x0f0f0000u, w << 12, bit_select(0xf0f00f0fu, w, w >> 12));
+  uint32_t t[4];
+  mx_unpack8(x, t);
+  h[0] = t[0];
+  h[2] = t[1];
+  h[1] = t[2];
+  h[3] = t[3];
+}
+
+// Codes of rows 16 u .. + 15 of a staged tile: per 8 rows i one word a block.
+// K (trans false): lane (g, c) gets word c of row 8 i + g; V: transposed.
+template <int D, int SWZ, bool TRANS>
+__device__ __forceinline__ void load_codes(const uint8_t* tile, int u, int lane,
+                                           uint32_t (&r)[2][D / 32]) {
+  constexpr int RB = D / 2;
+  auto ld = [](const uint8_t* p, uint32_t (&x)[4]) {
+    if constexpr (TRANS) ldsm_x4_trans(p, x);
+    else ldsm_x4(p, x);
+  };
+  if constexpr (D == 128) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int off = (16 * u + 8 * i + (lane & 7)) * RB + (lane >> 3) * 16;
+      ld(tile + (off ^ ((off >> 3) & SWZ)), r[i]);
+    }
+  } else {
+    uint32_t t[4];
+    const int off = (16 * u + 8 * (lane >> 4) + (lane & 7)) * RB + ((lane >> 3) & 1) * 16;
+    ld(tile + (off ^ ((off >> 3) & SWZ)), t);
+    r[0][0] = t[0];
+    r[0][1] = t[1];
+    r[1][0] = t[2];
+    r[1][1] = t[3];
+  }
+}
+
 // Nonzero if some byte of w is 255.
 __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return (~w - 0x01010101u) & w & 0x80808080u;
@@ -229,7 +285,7 @@ struct MxState {
   template <int SWZ>
   __device__ __forceinline__ void step(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
                                        const uint8_t* vs, int half, int valid, int lane) {
-    constexpr int RB = D / 2, SB = NB;
+    constexpr int SB = NB;
     constexpr unsigned FULL = 0xffffffffu;
     const int g = lane >> 2, c = lane & 3;
     // ---- logits: x[u][i][j] = token 16 u + 8 i + g, head 2 c + j
@@ -239,21 +295,7 @@ struct MxState {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t r[2][NB];  // [rows g / g + 8][block]
-      if constexpr (NB == 4) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int off = (16 * u + 8 * i + (lane & 7)) * RB + (lane >> 3) * 16;
-          ldsm_x4(kc + (off ^ ((off >> 3) & SWZ)), r[i]);
-        }
-      } else {
-        uint32_t t[4];
-        const int off = (16 * u + 8 * (lane >> 4) + (lane & 7)) * RB + ((lane >> 3) & 1) * 16;
-        ldsm_x4(kc + (off ^ ((off >> 3) & SWZ)), t);
-        r[0][0] = t[0];
-        r[0][1] = t[1];
-        r[1][0] = t[2];
-        r[1][1] = t[3];
-      }
+      load_codes<D, SWZ, false>(kc, u, lane, r);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         kw[u][i] = scale_word(ks + u * half + (8 * i + g) * SB);
@@ -373,21 +415,7 @@ struct MxState {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t r[2][NB];
-      if constexpr (NB == 4) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int off = (16 * u + 8 * i + (lane & 7)) * RB + (lane >> 3) * 16;
-          ldsm_x4_trans(vc + (off ^ ((off >> 3) & SWZ)), r[i]);
-        }
-      } else {
-        uint32_t t[4];
-        const int off = (16 * u + 8 * (lane >> 4) + (lane & 7)) * RB + ((lane >> 3) & 1) * 16;
-        ldsm_x4_trans(vc + (off ^ ((off >> 3) & SWZ)), t);
-        r[0][0] = t[0];
-        r[0][1] = t[1];
-        r[1][0] = t[2];
-        r[1][1] = t[3];
-      }
+      load_codes<D, SWZ, true>(vc, u, lane, r);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t f0 = f16_pow2(ex[u][0][b], ref[b]), f1 = f16_pow2(ex[u][1][b], ref[b]);
@@ -420,30 +448,6 @@ struct MxState {
         for (int i = 0; i < 2; ++i) bits |= (ex[u][i][b] + add) ^ 0x80008000u;
     }
     return bits & 0xfff0fff0u;
-  }
-
-  // f16 of 2^(v - r) for the halves v of x with max(r - below, 1) <= v <= r + 7,
-  // 0 for the others (a scale byte of 0 reads as 0).
-  static __device__ __forceinline__ uint32_t weights(uint32_t x, int r, int below) {
-    const int lo = max(r - below, 1);
-    const uint32_t in = halves_within(x, lo, r + 7);
-    const uint32_t keep = ((in & 0xffffu) ? 0x0000ffffu : 0u) | ((in >> 16) ? 0xffff0000u : 0u);
-    // the halves left out take the value r first: no carry into the other half
-    return f16_pow2(in | (static_cast<uint32_t>(max(r, 0)) * 0x10001u & ~keep), max(r, 0)) & keep;
-  }
-
-  // One word of V codes as ldmatrix.trans gives it (dims 4 g .. + 3 of tokens
-  // 2 c, 2 c + 1) -> per dim the f16 pair of the two tokens.
-  static __device__ __forceinline__ void v_pairs(uint32_t w, uint32_t (&h)[4]) {
-    // bytes: (token 2c, token 2c + 1) codes of dims 0, 2 and of dims 1, 3
-    const uint32_t t0 = (w & 0x0f0fu) | ((w >> 12) & 0xf0f0u);
-    const uint32_t t1 = ((w >> 4) & 0x0f0fu) | ((w >> 16) & 0xf0f0u);
-    uint32_t t[4];
-    mx_unpack8(prmt(t0, t1, 0x5410), t);
-    h[0] = t[0];
-    h[2] = t[1];
-    h[1] = t[2];
-    h[3] = t[3];
   }
 
   // The step's tokens whose V scale lies below the window of its block: bands
@@ -602,8 +606,331 @@ struct MxState {
   }
 };
 
-template <class QF, int D, int NW>
-__global__ void __launch_bounds__(NW * 32)
+// The same for kv-heads with few query heads (heads x blocks <= 8 columns of
+// N): column n is block n % NB of query head n / NB. For S the column's query
+// fragment is zero outside its block, so one chain of MMAs gives the partial
+// sums of all blocks, and lane (g, c) applies two scales to its two columns;
+// for O the column's P carries its block's scale, so a step needs one scaled P
+// instead of one per block (of O's columns those of a tile's own block count).
+// The scale work and the exponentials shrink by NB against MxState, where they
+// are a third of a step's instructions.
+template <class QF, int D>
+struct MxStateN {
+  static constexpr int NB = D / 32;
+  uint32_t q[NB][4];    // query fragments of column g: zero but in its block
+  float qs;             // base-2 logit scale of this lane's head (columns 2c, 2c+1)
+  float m, l;           // running maximum; this lane's part of the sum
+  float o[NB][2][4];    // O: block b, dims 32 b + 4 g + 2 i (+1) x columns 2c, 2c+1
+  int ref[NB];          // r_b: scale byte the V scales are taken relative to (-1: none yet)
+  int own;              // r_b of column g's block
+  uint32_t nan_blocks;
+  bool low;
+
+  static __device__ __forceinline__ int head_of(int col) { return col / NB; }
+
+  __device__ __forceinline__ void init(const DecodeArgs& a, const uint8_t* query, int group,
+                                       int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    const int hq = head_of(g), bq = g % NB;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4* row = reinterpret_cast<const uint4*>(query + static_cast<int64_t>(hq) * D * 2);
+    const uint4 w = hq < group ? row[bq * 4 + c] : zero;
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    int e = 0;  // power of two of this head's row
+    if constexpr (std::is_same<QF, BF16>::value) {
+      float mq = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = cvt2(BF16{}, x[j]);
+        mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+#pragma unroll
+      for (int d = 1; d < 4 * NB; d *= 2) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, d));
+      if (mq > 0.f && isfinite(mq)) e = -max(ilogbf(mq), -126);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = cvt2(BF16{}, x[j]);
+        const __half2 h = __floats2half2_rn(ldexpf(f.x, e), ldexpf(f.y, e));
+        x[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[b][j] = b == bq ? x[j] : 0u;
+      ref[b] = -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[b][i][j] = 0.f;
+    }
+    const int eh = __shfl_sync(0xffffffffu, e, head_of(2 * c) * NB * 4);
+    qs = a.scale_log2 * ldexpf(1.f, -(eh / 2)) * ldexpf(1.f, eh / 2 - eh);
+    m = -CUDART_INF_F;
+    l = 0.f;
+    own = -1;
+    nan_blocks = 0u;
+    low = true;
+  }
+
+  template <int SWZ>
+  __device__ __forceinline__ void step(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
+                                       const uint8_t* vs, int half, int valid, int lane) {
+    constexpr int SB = NB;
+    constexpr unsigned FULL = 0xffffffffu;
+    const int g = lane >> 2, c = lane & 3;
+    // ---- logits: x[u][i] = token 16 u + 8 i + g, the head of columns 2c, 2c+1
+    float x[2][2];
+    uint32_t ff[2][2], any_ff = 0u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t r[2][NB];
+      load_codes<D, SWZ, false>(kc, u, lane, r);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t h0[4], h1[4];
+        mx_unpack8(r[0][b], h0);
+        mx_unpack8(r[1][b], h1);
+        mma16816(s, h0[0], h1[0], h0[1], h1[1], q[b][0], q[b][1]);
+        mma16816(s, h0[2], h1[2], h0[3], h1[3], q[b][2], q[b][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // the scale bytes of this lane's two columns
+        uint32_t y = *reinterpret_cast<const uint16_t*>(ks + u * half + (8 * i + g) * SB +
+                                                        (2 * c) % NB);
+        if (valid < kStep && 16 * u + 8 * i + g >= valid) y = 0u;
+        ff[u][i] = has_ff(y);
+        any_ff |= ff[u][i];
+        const float f0 = __uint_as_float((y << 23) & 0x7f800000u);
+        const float f1 = __uint_as_float((y << 15) & 0x7f800000u);
+        x[u][i] = fmaf(f0, s[2 * i], f1 * s[2 * i + 1]);
+        if constexpr (NB == 4) x[u][i] += __shfl_xor_sync(FULL, x[u][i], 1);
+      }
+    }
+    // ---- V scales of column g's block, tokens 16 u + 8 i + 2 c, + 1 as halves
+    uint32_t ex[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* p = vs + u * half + (8 * i + 2 * c) * SB;
+        const uint32_t b = g % NB;
+        if constexpr (NB == 4) {
+          const uint2 t = *reinterpret_cast<const uint2*>(p);
+          ex[u][i] = prmt(t.x, t.y, b | (b + 4) << 8) & 0x00ff00ffu;
+        } else {
+          const uint32_t t = *reinterpret_cast<const uint32_t*>(p);
+          ex[u][i] = prmt(t, 0u, b | (b + 2) << 8) & 0x00ff00ffu;
+        }
+      }
+    float mx = -CUDART_INF_F;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float t = x[u][i] * qs;
+        if (valid < kStep && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
+        x[u][i] = t;
+        mx = fmaxf(mx, t);
+      }
+    if (valid < kStep) {  // rows that are not of the context: a scale within the window
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = valid - (16 * u + 8 * i + 2 * c);
+          const uint32_t keep = t <= 0 ? 0u : t == 1 ? 0x0000ffffu : 0xffffffffu;
+          ex[u][i] = (ex[u][i] & keep) | (static_cast<uint32_t>(max(own, 1)) * 0x10001u & ~keep);
+        }
+    }
+    const bool lift = mx > m + 8.f || outside(ex) || any_ff;
+    bool wide = low;  // (the same in every lane)
+    if (__any_sync(FULL, lift)) {
+      update(x, mx, ff, ex, lane);
+      wide = low || __any_sync(FULL, outside(ex));
+    }
+    // ---- probabilities, their sum, and P as B operand (tokens x columns)
+    const float mu = m == -CUDART_INF_F ? 0.f : m;
+    uint32_t p[2][2], pb[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float e = fast_ex2(x[u][i] - mu);
+        l += e;
+        const __half2 h = __floats2half2_rn(e, e);
+        p[u][i] = movm_trans(*reinterpret_cast<const uint32_t*>(&h));
+        const uint32_t f = wide ? weights(ex[u][i], own, 8) : f16_pow2(ex[u][i], own);
+        pb[u][i] = hmul2u(p[u][i], f);
+      }
+    // ---- O += V^T (P 2^(bV - r))
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t r[2][NB];
+      load_codes<D, SWZ, true>(vc, u, lane, r);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t h[2][4];
+        v_pairs(r[0][b], h[0]);
+        v_pairs(r[1][b], h[1]);
+        mma16816(o[b][0], h[0][0], h[0][1], h[1][0], h[1][1], pb[u][0], pb[u][1]);
+        mma16816(o[b][1], h[0][2], h[0][3], h[1][2], h[1][3], pb[u][0], pb[u][1]);
+      }
+    }
+    if (wide) bands<SWZ>(vc, p, ex, lane);
+  }
+
+  // Nonzero if a V scale of the step is not within [r_b - 8, r_b + 7].
+  __device__ __forceinline__ uint32_t outside(const uint32_t (&ex)[2][2]) const {
+    const uint32_t add = static_cast<uint32_t>(0x8000 + 8 - own) * 0x10001u;
+    return (((ex[0][0] + add) ^ 0x80008000u) | ((ex[0][1] + add) ^ 0x80008000u) |
+            ((ex[1][0] + add) ^ 0x80008000u) | ((ex[1][1] + add) ^ 0x80008000u)) &
+           0xfff0fff0u;
+  }
+
+  // Tokens whose V scale lies below the window: bands of 15 powers of two per
+  // block, from its largest such scale down (MxState::bands).
+  template <int SWZ>
+  __device__ __forceinline__ void bands(const uint8_t* vc, const uint32_t (&p)[2][2],
+                                        const uint32_t (&ex)[2][2], int lane) {
+    constexpr unsigned FULL = 0xffffffffu;
+    int hi = own - 9;
+    for (;;) {
+      int t = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t in = hi > 0 ? halves_within(ex[u][i], 1, hi) : 0u;
+          t = max(t, max(static_cast<int>(in & 0xffffu), static_cast<int>(in >> 16)));
+        }
+      t = max(t, __shfl_xor_sync(FULL, t, 1));
+      t = max(t, __shfl_xor_sync(FULL, t, 2));
+      if (!__any_sync(FULL, t > 0)) break;
+      float f[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int tb = __shfl_sync(FULL, t, b * 4);  // (column b is block b)
+        f[b] = tb > 0 ? pow2i(tb - ref[b]) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t r[2][NB];
+        load_codes<D, SWZ, true>(vc, u, lane, r);
+        const uint32_t b0 = t > 0 ? hmul2u(p[u][0], weights(halves_within(ex[u][0], 1, t), t, 14)) : 0u;
+        const uint32_t b1 = t > 0 ? hmul2u(p[u][1], weights(halves_within(ex[u][1], 1, t), t, 14)) : 0u;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t h[2][4];
+          v_pairs(r[0][b], h[0]);
+          v_pairs(r[1][b], h[1]);
+          float add[2][4] = {};
+          mma16816(add[0], h[0][0], h[0][1], h[1][0], h[1][1], b0, b1);
+          mma16816(add[1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[b][i][j] = fmaf(add[i][j], f[b], o[b][i][j]);
+        }
+      }
+      hi = t > 0 ? t - 15 : 0;
+    }
+  }
+
+  // MxState::update: maxima and references move, NaN scales are looked at.
+  __device__ __forceinline__ void update(float (&x)[2][2], float mx, const uint32_t (&ff)[2][2],
+                                         uint32_t (&ex)[2][2], int lane) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const int g = lane >> 2;
+    // a NaN K scale of any column makes the token's logit NaN for every head
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t bad = ff[u][i];
+        if constexpr (NB == 4) bad |= __shfl_xor_sync(FULL, bad, 1);
+        if (bad) x[u][i] = CUDART_NAN_F;
+      }
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
+    if (mx > m) {
+      const float f = m == -CUDART_INF_F ? 0.f : fast_ex2(m - mx);
+      l *= f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[b][i][j] *= f;
+      m = mx;
+    }
+    // references
+    int t = -1;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int v = (ex[u][i] >> (16 * j)) & 0xffff;
+          if (v == kMxNan) {
+            bad = true;
+            ex[u][i] &= j ? 0x0000ffffu : 0xffff0000u;  // as 0: no weight
+          } else {
+            t = max(t, v);
+          }
+        }
+    low = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const bool mine = g % NB == b;
+      if (__any_sync(FULL, mine && bad)) nan_blocks |= 1u << b;
+      const int tb = min(__reduce_max_sync(FULL, mine ? t : -1), 247);  // (MxState::update_scales)
+      if (tb > ref[b]) {
+        const float f = ref[b] < 0 ? 0.f : pow2i(ref[b] - tb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[b][i][j] *= f;
+        ref[b] = tb;
+      }
+      low |= ref[b] <= 8;
+      if (mine) own = ref[b];
+    }
+  }
+
+  __device__ __forceinline__ void finish(float* ml, float* ob, int group, int lane) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(FULL, l, d);
+    const int head = head_of(2 * c);
+    if (g == 0 && (2 * c) % NB == 0 && head < group) {
+      ml[2 * head] = m;
+      ml[2 * head + 1] = l;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float f = nan_blocks >> b & 1 ? CUDART_NAN_F
+                      : ref[b] <= 0       ? 0.f
+                                          : pow2i(ref[b] - 127);
+      // the lanes and the column that hold this block's own
+      if (head < group && (2 * c) % NB == (b & ~1)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            ob[head * D + 32 * b + 4 * g + 2 * i + k] = o[b][i][2 * k + (b & 1)] * f;
+      }
+    }
+  }
+};
+
+template <class QF, int D, int NW, bool BLOCKS_ON_N>
+__global__ void __launch_bounds__(NW * 32, BLOCKS_ON_N ? 4 : 3)
     paged_decode_mxfp4_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                               const __grid_constant__ CUtensorMap vmap,
                               const __grid_constant__ CUtensorMap ksmap,
@@ -694,7 +1021,7 @@ __global__ void __launch_bounds__(NW * 32)
     for (int k = 0; k < min(R, my_count); ++k) issue(k);
   }
 
-  MxState<QF, D> st;
+  typename std::conditional<BLOCKS_ON_N, MxStateN<QF, D>, MxState<QF, D>>::type st;
   const int64_t row0 = static_cast<int64_t>(s) * a.num_heads + kvh * group;
   st.init(a, static_cast<const uint8_t*>(a.query) + row0 * D * 2, group, lane);
   int k = 0;
@@ -769,13 +1096,13 @@ __global__ void __launch_bounds__(NW * 32)
   }
 }
 
-template <class QF, int D, int NW>
+template <class QF, int D, int NW, bool BLOCKS_ON_N>
 cudaError_t launch_mx(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t stream) {
   using C = MxCfg<D, NW>;
   if (a.partition_blocks > kMaxUnitBlocks || kStep % a.block_size != 0)
     return cudaErrorNotSupported;
   const size_t smem = 1024 + C::OFF_IDS + 4 * static_cast<size_t>(a.partition_blocks);
-  auto kern = paged_decode_mxfp4_kernel<QF, D, NW>;
+  auto kern = paged_decode_mxfp4_kernel<QF, D, NW, BLOCKS_ON_N>;
   cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.num_kv_heads, a.num_seqs, a.max_parts), NW * 32, smem, stream, a,
@@ -786,10 +1113,16 @@ cudaError_t launch_mx(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStr
 
 cudaError_t decode_mxfp4(const DecodeArgs& a, const CUtensorMap (&maps)[4], int q_dtype,
                          int head_dim, cudaStream_t stream) {
-  if (q_dtype == kF16 && head_dim == 64) return launch_mx<F16, 64, 4>(a, maps, stream);
-  if (q_dtype == kF16 && head_dim == 128) return launch_mx<F16, 128, 4>(a, maps, stream);
-  if (q_dtype == kBF16 && head_dim == 64) return launch_mx<BF16, 64, 4>(a, maps, stream);
-  if (q_dtype == kBF16 && head_dim == 128) return launch_mx<BF16, 128, 4>(a, maps, stream);
+  const int group = a.num_heads / a.num_kv_heads;
+  const bool n = group * (head_dim / 32) <= 8;
+#define PAGED_MX(QT, QF, d)                                                     \
+  if (q_dtype == QT && head_dim == d)                                          \
+    return n ? launch_mx<QF, d, 4, true>(a, maps, stream) : launch_mx<QF, d, 4, false>(a, maps, stream);
+  PAGED_MX(kF16, F16, 64)
+  PAGED_MX(kF16, F16, 128)
+  PAGED_MX(kBF16, BF16, 64)
+  PAGED_MX(kBF16, BF16, 128)
+#undef PAGED_MX
   return cudaErrorNotSupported;
 }
 

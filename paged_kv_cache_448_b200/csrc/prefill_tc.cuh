@@ -44,12 +44,19 @@
 // 8-bit MMAs per K step; P (<= 2^8 under the lazy maximum) goes to tensor
 // memory as an E4M3 hi part and an E5M2 residual, so O += P V takes two
 // 8-bit MMAs with V read MN-major; the V scale applies in the epilogue.
-// An MXFP4 cache (mxfp4.cuh) is widened to the query's type on its way into
-// shared memory: in place of the TMA warps, seven converter warps load codes
-// and scales into registers, some items ahead (an item is 32 blocks of 32
-// codes: 8 rows of 128 dims), and once the MMAs that read a stage completed
-// they write code * 2^(b - 127) into it in the layout the TMA boxes have. From
-// there on it is the 16-bit kernel. The warps take the items of K and V in one
+// An MXFP4 cache (mxfp4.cuh) is widened to f16 on its way into shared memory:
+// in place of the TMA warps, seven converter warps load codes and scales into
+// registers, some items ahead (an item is 16 rows), and once the MMAs that read a stage completed they write
+// code * 2^(b - r + 13) into it in the layout the TMA boxes have. From there on
+// it is the f16 kernel. r is a reference for the scales, undone in the logit
+// scale and the epilogue: with an f16 query 140 (the values themselves), with a
+// bf16 query the largest scale byte among the CTA's keys (values), so that
+// every value down to 2^-36 of the largest is exact in f16; it is found by
+// reading the scale bytes once before the pipeline starts. (Widening to bf16
+// needs no reference, but three times the instructions of the conversion to
+// f16, which are what bounds the kernel, and P in two parts: 8 draft tokens x
+// 8 heads of 64 sequences took 202 us.) A bf16 query row is scaled by a power
+// of two that puts its largest element in [1, 2). The warps take the items of K and V in one
 // order, K a step ahead of V; a stage is full when each of its items arrived.
 // The register file is shared out anew once the roles are known (softmax
 // warps more, the others less).
@@ -97,15 +104,16 @@ struct TcCfg {
   static constexpr int H = NT / 64;                  // 64-token halves of a step
   static constexpr bool FP8 = CF::kBytes == 1;
   static constexpr bool MX = std::is_same<CF, Mxfp4>::value;
-  static constexpr bool BF = std::is_same<QF, BF16>::value;
+  static constexpr bool OBF = std::is_same<QF, BF16>::value;  // query and output
+  static constexpr bool BF = OBF && !MX;                      // MMA operands
   // warps besides the softmax warps: MMA issue, then the loaders
   static constexpr int CW = MX ? 7 : 2;
   static constexpr int THREADS = NG * kTcRows + 32 + 32 * CW;
   // MXFP4: registers per thread at launch (what __launch_bounds__ leaves), of
   // the softmax warps and of the other eight; the same total before and after
   static constexpr int LAUNCH_REGS = NG == 2 ? 128 : 80;
-  static constexpr int SOFTMAX_REGS = NG == 2 ? 168 : 128;
-  static constexpr int OTHER_REGS = NG == 2 ? 88 : 56;
+  static constexpr int SOFTMAX_REGS = NG == 2 ? 168 : 112;
+  static constexpr int OTHER_REGS = NG == 2 ? 88 : 64;
   static_assert(!MX || (NG * kTcRows * SOFTMAX_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS &&
                         THREADS == NG * kTcRows + 256),
                 "register shares");
@@ -178,6 +186,28 @@ __device__ __forceinline__ float2 unpack_q(uint32_t w) {
   return __half22float2(h);
 }
 
+// Largest magnitude of eight bf16 values, and the values times 2^e as f16.
+__device__ __forceinline__ float chunk_max(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_q<BF16>(w[j]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return m;
+}
+__device__ __forceinline__ uint4 scaled_f16(const uint4& v, int e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_q<BF16>(w[j]);
+    o[j] = pack2<false>(ldexpf(f.x, e), ldexpf(f.y, e));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 constexpr int kOrderSeqs = 256;  // launches of up to this many sequences are reordered
 
 // The sequence of rank `rank` when the sequences are ordered by context length,
@@ -216,91 +246,49 @@ struct TcCache<Mxfp4> {
   const uint8_t* scales[2];
 };
 
-// 32 codes of one block and their scale byte -> 32 values of the query's type
-// (rounded to nearest), four 16-byte chunks of 8 dims.
-//  * f16: a power of two 2^(b - 127) from 2^-24 to 2^13, so that no product
-//    overflows; below it 0, above it 2^13. Exact for caches written from f16
-//    rows, but for codes below f16's own resolution.
-//  * bf16: the code's three magnitude bits placed over the exponent's lowest
-//    two bits and the mantissa's highest are the value times 2^-126 (E2M1's
-//    subnormal 0.5 included); 2^100 and 2^(b - 101) undo it and apply the
-//    scale (exact; scales above 2^101 in a third factor). This takes half the
-//    integer instructions of converting to f16 first and moving the fields,
-//    and leaves the dims of a chunk in the order 0 4 1 5 2 6 3 7, which Q's
-//    chunks follow (permute_chunk) and the epilogue undoes for V (chunk_at).
-template <bool BF>
-__device__ __forceinline__ void mx_widen(const uint4& codes, int b, uint4 (&out)[4]) {
+// Scale reference that leaves the values as they are (2^(b - 127) = 2^(b - r + 13)).
+constexpr int kMxTrueRef = 140;
+
+// 32 codes of one block and their scale byte b <= r -> f16 of code * 2^(b - r + 13)
+// (nearest), four 16-byte chunks of 8 dims. Scales above the reference are
+// taken as the reference (no product overflows), a byte of 0 reads as 0.
+__device__ __forceinline__ void mx_widen(const uint4& codes, int b, int r, uint4 (&out)[4]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t f;
-  if constexpr (BF) {
-    f = b == kMxNan ? 0x7fc0u : b == 0 ? 0u : static_cast<uint32_t>(min(b + 26, 254)) << 7;
-  } else {
-    f = b == kMxNan ? 0x7e00u
-        : b > 112   ? static_cast<uint32_t>(min(b, 140) - 112) << 10
-        : b > 102   ? 1u << (b - 103)
-                    : 0u;
-  }
+  const int field = min(b, r) - r + 28;  // f16 exponent field of the factor
+  uint32_t f = field > 0 ? static_cast<uint32_t>(field) << 10 : field > -10 ? 512u >> -field : 0u;
+  if (b == 0) f = 0u;
+  if (b == kMxNan) f = 0x7e00u;
   f *= 0x10001u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t o[4];
-    if constexpr (BF) {
-      auto mul = [](uint32_t x, uint32_t y) {
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&y));
-        return *reinterpret_cast<const uint32_t*>(&r);
-      };
-      // nibbles j and j + 4, one in each half: magnitude at bits 6-8, sign at 15
-      const uint32_t m[4] = {w[i] << 6, w[i] << 2, w[i] >> 2, w[i] >> 6};
-      const uint32_t sg[4] = {w[i] << 12, w[i] << 8, w[i] << 4, w[i]};
+    uint32_t h[4], o[4];
+    mx_unpack8(w[i], h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t t = (m[j] & 0x01c001c0u) | (sg[j] & 0x80008000u);
-        o[j] = mul(mul(t, 0x71807180u), f);  // 0x7180: 2^100
-      }
-      if (b > 228 && b != kMxNan) {
-        const uint32_t f2 = static_cast<uint32_t>((b - 228 + 127) << 7) * 0x10001u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = mul(o[j], f2);
-      }
-    } else {
-      uint32_t h[4];
-      mx_unpack8(w[i], h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[j]),
-                                  *reinterpret_cast<const __half2*>(&f));
-        o[j] = *reinterpret_cast<const uint32_t*>(&r);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[j]),
+                                *reinterpret_cast<const __half2*>(&f));
+      o[j] = *reinterpret_cast<const uint32_t*>(&r);
     }
     out[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-// A chunk of 8 16-bit values in the order mx_widen leaves bf16 values in.
-__device__ __forceinline__ uint4 permute_chunk(const uint4& v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-}
-
-// Column of dim d (0..7) within a chunk of 8: as stored, or in that order.
-template <bool PERMUTED>
-__host__ __device__ constexpr int chunk_at(int d) {
-  return PERMUTED ? (d < 4 ? 2 * d : 2 * (d - 4) + 1) : d;
-}
-
-// One converter lane's share of an item: 32 codes and their scale byte.
+// One converter lane's share of an item: per load 32 codes and their scale byte.
+template <int SUB>
 struct MxRaw {
-  uint4 codes;
-  uint32_t scale;
+  uint4 codes[SUB];
+  uint32_t scale[SUB];
 };
 
-__device__ __forceinline__ void mx_load(MxRaw& raw, const uint8_t* codes, const uint8_t* scale) {
+template <int SUB>
+__device__ __forceinline__ void mx_load(MxRaw<SUB>& raw, int u, const uint8_t* codes,
+                                        const uint8_t* scale) {
   asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(raw.codes.x), "=r"(raw.codes.y), "=r"(raw.codes.z), "=r"(raw.codes.w)
+               : "=r"(raw.codes[u].x), "=r"(raw.codes[u].y), "=r"(raw.codes[u].z),
+                 "=r"(raw.codes[u].w)
                : "l"(codes)
                : "memory");
-  asm volatile("ld.global.cg.u8 %0, [%1];" : "=r"(raw.scale) : "l"(scale) : "memory");
+  asm volatile("ld.global.cg.u8 %0, [%1];" : "=r"(raw.scale[u]) : "l"(scale) : "memory");
 }
 
 template <class QF, class CF, int D, int G, int NG>
@@ -334,11 +322,11 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const uint64_t lim = a.wait_limit_ns;
   if (tid == 0) {
     for (int r = 0; r < KR; ++r) {
-      mbar_init(&kfull[r], MX ? NT / (1024 / D) : 1);
+      mbar_init(&kfull[r], MX ? NT / TR : 1);
       mbar_init(&kempty[r], 1);
     }
     for (int r = 0; r < VR; ++r) {
-      mbar_init(&vfull[r], MX ? NT / (1024 / D) : 1);
+      mbar_init(&vfull[r], MX ? NT / TR : 1);
       mbar_init(&vempty[r], 1);
     }
     for (int g = 0; g < NG; ++g)
@@ -418,7 +406,47 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const int kbase = tbase / (NT / TR);
   const int nsteps = (tend - tbase + NT / TR - 1) / (NT / TR);
 
+  // MXFP4, bf16 query: the largest scale bytes of this CTA's keys and values
+  // (255, a NaN block, aside; bytes of rows that are not there do not count)
+  __shared__ int ref_part[2][C::THREADS / 32];
+  if constexpr (MX && C::OBF) {
+    const int kv_end = min(ctx, tend * TR);
+    const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+    const int bs_log = a.block_size == 32 ? 5 : 4;
+    int top[2] = {0, 0};
+    for (int t = tbase * TR + tid; t < kv_end; t += C::THREADS) {
+      const int32_t id = table[t >> bs_log];
+      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.num_blocks)) continue;
+      const int64_t row = (static_cast<int64_t>(id) * a.num_kv_heads + kvh) * a.block_size +
+                          (t & (a.block_size - 1));
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint8_t* p = cache.scales[v] + row * (D / 32);
+        const uint32_t w = D == 128 ? __ldcg(reinterpret_cast<const uint32_t*>(p))
+                                    : __ldcg(reinterpret_cast<const uint16_t*>(p));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int b = (w >> (8 * i)) & 255;
+          if (b != kMxNan) top[v] = max(top[v], b);
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      top[v] = __reduce_max_sync(0xffffffffu, top[v]);
+      if (lane == 0) ref_part[v][warp] = top[v];
+    }
+  }
   __syncthreads();  // barrier initialisation visible to every thread
+  int ref_k = kMxTrueRef, ref_v = kMxTrueRef;
+  if constexpr (MX && C::OBF) {
+    ref_k = ref_v = 0;
+#pragma unroll
+    for (int i = 0; i < C::THREADS / 32; ++i) {
+      ref_k = max(ref_k, ref_part[0][i]);
+      ref_v = max(ref_v, ref_part[1][i]);
+    }
+  }
   if (warp == kMma) tc::alloc(&tmem_slot, C::TMEM_COLS);
   float qscale = a.scale_log2;  // logit scale of this thread's row (base 2)
   if (warp < kMma) {
@@ -426,13 +454,32 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     const int g = tid / kTcRows, rr = tid % kTcRows;
     const uint4* q4 = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.query) +
                                                      row_off * 2);
-    if constexpr (!FP8) {
+    if constexpr (MX) {
+      int qe = 0;
+      if constexpr (C::OBF) {
+        float mq = 0.f;
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) mq = fmaxf(mq, chunk_max(q4[c]));
+        }
+        if (mq > 0.f && isfinite(mq)) qe = -max(ilogbf(mq), -126);
+      }
+      // (the exponents together: each alone may leave fp32's range)
+      qscale = ldexpf(qscale, ref_k - kMxTrueRef - qe);
 #pragma unroll
       for (int sg = 0; sg < NSEG; ++sg)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (MX && BF) v = permute_chunk(v);
+          if constexpr (C::OBF) v = scaled_f16(v, qe);
+          *reinterpret_cast<uint4*>(sq(g) + sg * C::QPART + sw128(rr, c)) = v;
+        }
+    } else if constexpr (!FP8) {
+#pragma unroll
+      for (int sg = 0; sg < NSEG; ++sg)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
           *reinterpret_cast<uint4*>(sq(g) + sg * C::QPART + sw128(rr, c)) = v;
         }
     } else {
@@ -489,51 +536,55 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   if (MX && warp >= kLoader) {
     if constexpr (MX) {
       // ================= converter warps =================
-      constexpr int NB = D / 32, RPI = 32 / NB;  // blocks of a row, rows of an item
-      constexpr int ITEMS = NT / RPI;            // items of a stage
-      constexpr int AHEAD = 4;                   // items in flight per warp
-      static_assert(16 % RPI == 0 && (ITEMS & (ITEMS - 1)) == 0, "an item within one block");
+      constexpr int NB = D / 32, RPL = 32 / NB;  // blocks of a row, rows of one load
+      constexpr int SUB = TR / RPL;              // loads of an item (16 rows)
+      constexpr int ITEMS = NT / TR;             // items of a stage
+      constexpr int AHEAD = SUB == 2 ? 2 : 4;    // items in flight per warp
+      static_assert((ITEMS & (ITEMS - 1)) == 0, "whole chunks");
       const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
       const int bs_log = a.block_size == 32 ? 5 : 4;
       const int kv_end = min(ctx, tend * TR);  // end of this CTA's tokens
-      // lane -> (row of the item, block): eight lanes that store together
+      // lane -> (row of the load, block): eight lanes that store together
       // write four rows x two blocks of one segment, in eight different
       // 16-byte columns of the swizzled tile
       const int lb = NB == 4 ? (lane >> 4) * 2 + (lane & 1) : (lane & 1);
       const int lr = NB == 4 ? (lane >> 1) & 7 : lane >> 1;
       // Item n of the CTA is item n % ITEMS of chunk c = n / ITEMS, the chunks
       // in the order K0, K1 V0, K2 V1, ... (the K past the last step is empty).
+      // All of this is the same in a warp's lanes.
       auto is_v = [](uint32_t n) { return n >= 2 * ITEMS && ((n / ITEMS) & 1) == 0; };
       auto step_of = [&](uint32_t n) {
-        const int c = static_cast<int>(n / ITEMS);
-        return is_v(n) ? c / 2 - 1 : (c + 1) / 2;
+        return static_cast<int>((n / ITEMS + 1) / 2) - (is_v(n) ? 1 : 0);
       };
       const uint32_t total = (2 * nsteps + 1) * ITEMS;
       auto token = [&](uint32_t n) {
-        return (kbase + step_of(n)) * NT + static_cast<int>(n % ITEMS) * RPI;
+        return (kbase + step_of(n)) * NT + static_cast<int>(n % ITEMS) * TR;
       };
-      // block id of item n, INT32_MAX where it has no tokens
-      auto load_id = [&](uint32_t n) {
+      // block id of item n (of the last block where it has no tokens): a plain
+      // load, whose value is first looked at when the item's rows are loaded
+      auto load_id = [&](uint32_t n) { return __ldg(table + (min(token(n), kv_end - 1) >> bs_log)); };
+      // loads of item n, whose block is id; returns how many of its rows there
+      // are (rows past them read block 0, and get the scale byte 0 when used)
+      const int32_t cstride = a.num_kv_heads * a.block_size * (D / 2);  // bytes of a block
+      const int32_t sstride = a.num_kv_heads * a.block_size * NB;
+      const int32_t coff = (kvh * a.block_size + lr) * (D / 2) + lb * 16;
+      const int32_t soff = (kvh * a.block_size + lr) * NB + lb;
+      const uint32_t pool = static_cast<uint32_t>(a.num_blocks);
+      auto load = [&](uint32_t n, int32_t id, MxRaw<SUB>& raw) {
         const int t = token(n);
-        if (n >= total || t >= kv_end) return INT32_MAX;
-        const int32_t b = __ldg(table + (t >> bs_log));
-        return b;
-      };
-      // loads of item n, whose block is id; a row that is not there reads block 0
-      // and is given the scale byte 0 when it is used
-      auto load = [&](uint32_t n, int32_t id, MxRaw& raw) {
-        const int t = token(n) + lr;
-        const bool there = id >= 0 && id < a.num_blocks && t < kv_end && n < total;
-        if (!there && lane == 0 && n < total && t < kv_end) report(a.err, kErrBadBlockId);
-        const int64_t row =
-            ((there ? static_cast<int64_t>(id) : 0) * a.num_kv_heads + kvh) * a.block_size +
-            (t & (a.block_size - 1));
-        const int v = is_v(n);
-        mx_load(raw, cache.codes[v] + row * (D / 2) + lb * 16, cache.scales[v] + row * NB + lb);
-        return there;
+        const bool real = n < total && t < kv_end, known = static_cast<uint32_t>(id) < pool;
+        if (real && !known && lane == 0) report(a.err, kErrBadBlockId);
+        const int64_t b = known ? id : 0;
+        const int row = static_cast<int>(n % ITEMS) * TR & (a.block_size - 1);
+        const bool v = is_v(n);
+        const uint8_t* c = (v ? cache.codes[1] : cache.codes[0]) + (b * cstride + (coff + row * (D / 2)));
+        const uint8_t* sc = (v ? cache.scales[1] : cache.scales[0]) + (b * sstride + (soff + row * NB));
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) mx_load(raw, u, c + u * RPL * (D / 2), sc + u * RPL * NB);
+        return real && known ? kv_end - t : 0;
       };
       bool ok = true;
-      auto convert = [&](uint32_t n, const MxRaw& raw, bool there) {
+      auto convert = [&](uint32_t n, const MxRaw<SUB>& raw, int rows) {
         const int k = step_of(n), j = static_cast<int>(n % ITEMS);
         if (k >= nsteps) return;  // (the K past the last step)
         const bool v = is_v(n);
@@ -546,28 +597,32 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
         if (!v && a.skip_tile >= t_begin - tbase && a.skip_tile < t_end - tbase &&
             skip_unit_for_test(a.skip_tile, a.skip_tile, first_unit))
           return;  // (the step is never complete)
-        uint4 o[4];
-        mx_widen<BF>(raw.codes, there ? static_cast<int>(raw.scale) : 0, o);
-        const int r = j * RPI + lr;
         uint8_t* seg = (v ? sv(k) : sk(k)) + (lb / 2) * C::KV_SEG;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(seg + sw128(r, (lb & 1) * 4 + i)) = o[i];
+        for (int u = 0; u < SUB; ++u) {
+          const int r = u * RPL + lr;
+          uint4 o[4];
+          mx_widen(raw.codes[u], r < rows ? static_cast<int>(raw.scale[u]) : 0, v ? ref_v : ref_k,
+                   o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(seg + sw128(j * TR + r, (lb & 1) * 4 + i)) = o[i];
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v ? &vfull[k % VR] : &kfull[k % KR]);
       };
       // this warp's items are w, w + CW, ...; slot i of the rotating registers
       // holds the loads of item n + i CW, and the block id of item n + (i + AHEAD) CW
-      MxRaw raw[AHEAD];
-      bool there[AHEAD];
+      MxRaw<SUB> raw[AHEAD];
+      int rows[AHEAD];
       int32_t id[AHEAD];
-      uint32_t n = warp - kLoader;
+      uint32_t n = __shfl_sync(0xffffffffu, warp, 0) - kLoader;
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) id[i] = load_id(n + i * C::CW);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        there[i] = load(n + i * C::CW, id[i], raw[i]);
+        rows[i] = load(n + i * C::CW, id[i], raw[i]);
         id[i] = load_id(n + (i + AHEAD) * C::CW);
       }
       for (; ok && n < total; n += AHEAD * C::CW) {
@@ -575,8 +630,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
         for (int i = 0; i < AHEAD; ++i) {
           const uint32_t m = n + i * C::CW;
           if (!ok || m >= total) break;
-          convert(m, raw[i], there[i]);
-          there[i] = load(m + AHEAD * C::CW, id[i], raw[i]);
+          convert(m, raw[i], rows[i]);
+          rows[i] = load(m + AHEAD * C::CW, id[i], raw[i]);
           id[i] = load_id(m + 2 * AHEAD * C::CW);
         }
       }
@@ -1086,8 +1141,14 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // a split key range, (max, sum) and O / l in fp32 for the combine
       // kernel (a row that sees none of the part's tokens leaves -inf, 0, 0)
       tc::fence_after_sync();
-      auto at = [](int d) { return d / 8 * 8 + chunk_at<MX && BF>(d % 8); };  // column of a dim
       const float inv = (l > 0.f ? 1.f / l : 0.f) * (FP8 ? a.v_scale[kvh] : 1.f);
+      // MXFP4, bf16 query: V's reference, after the division (together they
+      // may leave fp32's range)
+      const float vref = MX && C::OBF ? ldexpf(1.f, max(ref_v - kMxTrueRef, -126)) : 1.f;
+      auto res = [&](float x) {
+        if constexpr (MX && C::OBF) return x * inv * vref;
+        else return x * inv;
+      };
       if (parts == 1) {
         uint4* o4 = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row_off * 2);
 #pragma unroll
@@ -1101,10 +1162,11 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
           if (out_row) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              o4[c * 4 + q] = make_uint4(pack_pair(BF, o[at(8 * q)] * inv, o[at(8 * q + 1)] * inv),
-                                         pack_pair(BF, o[at(8 * q + 2)] * inv, o[at(8 * q + 3)] * inv),
-                                         pack_pair(BF, o[at(8 * q + 4)] * inv, o[at(8 * q + 5)] * inv),
-                                         pack_pair(BF, o[at(8 * q + 6)] * inv, o[at(8 * q + 7)] * inv));
+              o4[c * 4 + q] =
+                  make_uint4(pack_pair(C::OBF, res(o[8 * q]), res(o[8 * q + 1])),
+                             pack_pair(C::OBF, res(o[8 * q + 2]), res(o[8 * q + 3])),
+                             pack_pair(C::OBF, res(o[8 * q + 4]), res(o[8 * q + 5])),
+                             pack_pair(C::OBF, res(o[8 * q + 6]), res(o[8 * q + 7])));
           }
         }
       } else {
@@ -1122,8 +1184,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
           if (out_row) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              w4[c * 8 + q] = make_float4(o[at(4 * q)] * inv, o[at(4 * q + 1)] * inv,
-                                          o[at(4 * q + 2)] * inv, o[at(4 * q + 3)] * inv);
+              w4[c * 8 + q] = make_float4(res(o[4 * q]), res(o[4 * q + 1]), res(o[4 * q + 2]),
+                                          res(o[4 * q + 3]));
           }
         }
       }

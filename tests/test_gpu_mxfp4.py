@@ -379,7 +379,7 @@ def test_chunks_whose_rows_maxima_grow_apart(Hkv, group, D, dtype, n, qlen):
 
 
 def test_chunks_bf16_full_range():
-    """A bf16 query takes every scale the format has."""
+    """A bf16 query takes every scale the format has, and values down to 2^-36 of the largest."""
     rng = np.random.default_rng(23)
     for e in (-110, -30, 30, 100):
         cache = mx.Cache([60, 130], 1, 128, 16, rng,
@@ -389,6 +389,28 @@ def test_chunks_bf16_full_range():
         out, _ = run_chunk(q, cache, [30, 60], 0.1)
         ref, bound = mx.attention(qx, cache, [30, 60], 0.1, "bf16")
         mx.check(out, ref, bound, f"query 2^{e}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("qlen", [3, 100, 300])
+def test_chunks_bf16_large_value_with_no_weight(D, qlen):
+    """One value 2^20 times the others whose weight is next to nothing: the others' sum keeps its
+    accuracy (2^-17 of them: f16's 2^-11, its exponent's 36 powers of two less the 20)."""
+    rng = np.random.default_rng(28)
+    cache = mx.Cache([400], 1, D, 16, rng, spare=0)
+    at = (int(cache.table[0, 3]), 0, 7)
+    cache.vs[at] = 147
+    c, sc = mx.encode(np.full((1, D), -4.0))
+    cache.kc[at], cache.ks[at] = c[0], sc[0]
+    q = torch.ones(qlen, 1, D, dtype=torch.bfloat16, device="cuda")
+    scale = 40.0 / (4 * D)
+    out, _ = run_chunk(q, cache, [qlen], scale)
+    ref, bound = mx.attention(np.ones((qlen, 1, D)), cache, [qlen], scale, "bf16")
+    others = np.abs(np.delete(cache.rows(0)[1][0], 3 * 16 + 7, 0)).max(0)
+    # the large value's weight is below e^-38 / 100; the rest as for the others alone
+    bound = (mx.HALF_STEP["bf16"] * np.abs(ref) + (2.0 ** -11 + 2.0 ** -13) * others +
+             400 * 2.0 ** -24 * others + math.exp(-38) * 2.0 ** 23)
+    mx.check(out, ref, bound, "large value")
 
 
 def test_chunks_f16_range():
