@@ -401,7 +401,8 @@ PA_API pa_status pa_gather_cache_mxfp4(void* key, void* value, const uint8_t* ke
 /*
  * pa_decode over an MXFP4 cache: the same operation, arguments, limits,
  * workspace (pa_decode_workspace_size with PA_MXFP4) and run-time table
- * errors; q_dtype F16 or BF16. A NaN block of K makes the output rows of its
+ * errors; q_dtype F16 or BF16. It has no pipeline wait that could run out, so a
+ * request of pa_inject_wait_timeout is used up without effect. A NaN block of K makes the output rows of its
  * kv-head NaN, one of V the 32 outputs it belongs to.
  */
 PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* key_cache,

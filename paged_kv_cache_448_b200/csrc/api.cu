@@ -92,59 +92,6 @@ pa_status encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_bloc
   return PA_OK;
 }
 
-// Tensor maps over an MXFP4 cache (mxfp4.cuh). Codes: [num_blocks][kv-heads x
-// block_size rows][head_dim / 2 bytes], one box = one kv-head's rows of a block,
-// swizzled by the row's width. Scales: [num_blocks][kv-heads x block_size x
-// head_dim / 32 bytes], one box = the bytes of one kv-head.
-pa_status encode_mxfp4_codes(CUtensorMap* map, const void* codes, int64_t num_blocks,
-                             int32_t block_size, int32_t hkv, int32_t head_dim) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t rb = static_cast<cuuint64_t>(head_dim) / 2;
-  const cuuint64_t rows = static_cast<cuuint64_t>(hkv) * block_size;
-  cuuint64_t dims[3] = {rb, rows, static_cast<cuuint64_t>(num_blocks)};
-  cuuint64_t strides[2] = {rb, rb * rows};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(rb), static_cast<cuuint32_t>(block_size), 1u};
-  cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
-  return PA_OK;
-}
-
-pa_status encode_mxfp4_scales(CUtensorMap* map, const void* scales, int64_t num_blocks,
-                              int32_t block_size, int32_t hkv, int32_t head_dim) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t per_head = static_cast<cuuint32_t>(block_size) * (head_dim / 32);
-  const cuuint64_t per_block = static_cast<cuuint64_t>(hkv) * per_head;
-  cuuint64_t dims[2] = {per_block, static_cast<cuuint64_t>(num_blocks)};
-  cuuint64_t strides[1] = {per_block};
-  cuuint32_t box[2] = {per_head, 1u};
-  cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(scales), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
-  return PA_OK;
-}
-
-// All four planes of an MXFP4 cache: K codes, V codes, K scales, V scales.
-pa_status encode_mxfp4(CUtensorMap (&maps)[4], const uint8_t* kc, const uint8_t* vc,
-                       const uint8_t* ks, const uint8_t* vs, int64_t num_blocks,
-                       int32_t block_size, int32_t hkv, int32_t head_dim) {
-  pa_status st = encode_mxfp4_codes(&maps[0], kc, num_blocks, block_size, hkv, head_dim);
-  if (st == PA_OK)
-    st = encode_mxfp4_codes(&maps[1], vc, num_blocks, block_size, hkv, head_dim);
-  if (st == PA_OK)
-    st = encode_mxfp4_scales(&maps[2], ks, num_blocks, block_size, hkv, head_dim);
-  if (st == PA_OK)
-    st = encode_mxfp4_scales(&maps[3], vs, num_blocks, block_size, hkv, head_dim);
-  return st;
-}
-
 pa_status cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return PA_OK;
   if (e == cudaErrorNotSupported)
@@ -169,8 +116,13 @@ constexpr int32_t kMaxParts = 65535;  // partitions per sequence (grid z extent)
 // 1 500 tokens), one pass 77 us against 98 / 120 / 175 us with partitions of
 // 1 024 / 512 / 256 tokens. It is cut into partitions only below one wave of
 // units. The other decode kernels (three CTAs per SM) want about four waves.
+// The MXFP4 kernel (four CTAs per SM) is cut only where the sequences x
+// kv-heads are below one wave, then like the others: 1 024 units of 2 048
+// tokens 69 us in one pass, 74 / 82 us with partitions of 1 024 / 512; 192
+// units of 1 024 to 32 768 tokens 99 us with 2 048, 107 / 112 us with 4 096 /
+// 1 024.
 Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
-               int32_t max_context_len, int32_t requested, bool fp8_tc) {
+               int32_t max_context_len, int32_t requested, bool fp8_tc, bool mxfp4 = false) {
   const int32_t blocks_max = std::max<int32_t>(1, (max_context_len + block_size - 1) / block_size);
   Plan p{};
   int32_t pb;
@@ -182,7 +134,7 @@ Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
     const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
     const int64_t want = fp8_tc ? 2LL * sm_count() : 4LL * sm_count() * 3;
     pb = blocks_max;
-    if (pairs < want && static_cast<int64_t>(blocks_max) * block_size > kMinAutoPartition) {
+    if (pairs < (mxfp4 ? 4LL * sm_count() : want) && static_cast<int64_t>(blocks_max) * block_size > kMinAutoPartition) {
       const int32_t min_pb = std::max(1, kMinAutoPartition / block_size);
       pb = min_pb;
       // largest power-of-two multiple of the minimum that still gives `want` units
@@ -310,7 +262,7 @@ PA_API int32_t pa_decode_partition_tokens(int32_t num_seqs, int32_t num_heads,
   (void)num_heads;
   if (num_seqs < 0 || num_kv_heads <= 0 || block_size <= 0 || max_context_len < 0) return 0;
   Plan p = make_plan(num_seqs, num_kv_heads, block_size, max_context_len, partition_tokens,
-                     cache_dtype == PA_FP8_E4M3 && head_dim == 128);
+                     cache_dtype == PA_FP8_E4M3 && head_dim == 128, cache_dtype == PA_MXFP4);
   return p.max_parts <= 1 ? std::max(p.partition_tokens, max_context_len) : p.partition_tokens;
 }
 
@@ -322,7 +274,7 @@ PA_API size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int3
       max_context_len < 0)
     return 0;
   Plan p = make_plan(num_seqs, num_kv_heads, block_size, max_context_len, partition_tokens,
-                     cache_dtype == PA_FP8_E4M3 && head_dim == 128);
+                     cache_dtype == PA_FP8_E4M3 && head_dim == 128, cache_dtype == PA_MXFP4);
   (void)num_kv_heads;
   return layout_for(p, num_seqs, num_heads, head_dim).total;
 }
@@ -820,7 +772,7 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
                 head_dim, block_size);
   if (q_dtype != PA_F16 && q_dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: query must be f16 or bf16");
-  if (num_blocks > INT32_MAX || static_cast<int64_t>(num_kv_heads) * block_size > INT32_MAX / 4)
+  if (num_blocks > INT32_MAX || static_cast<int64_t>(num_kv_heads) * block_size > INT32_MAX / 64)
     return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: pool or block too large");
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: scale is not finite");
   if (!workspace || !aligned(workspace, 256))
@@ -835,7 +787,7 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
     return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: misaligned pointer");
 
   const Plan plan = make_plan(num_seqs, num_kv_heads, block_size, max_context_len,
-                              partition_tokens, false);
+                              partition_tokens, false, true);
   if (num_seqs > 65535 || plan.max_parts > kMaxParts)
     return fail(PA_ERR_UNSUPPORTED, "decode_mxfp4: %d sequences x %d partitions exceed the grid",
                 num_seqs, plan.max_parts);
@@ -843,11 +795,6 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
   if (workspace_bytes < lay.total)
     return fail(PA_ERR_INVALID_ARG, "decode_mxfp4: workspace %zu bytes < %zu needed",
                 workspace_bytes, lay.total);
-  CUtensorMap maps[4];
-  pa_status st = encode_mxfp4(maps, key_cache, value_cache, k_scales, v_scales, num_blocks,
-                              block_size, num_kv_heads, head_dim);
-  if (st != PA_OK) return st;
-
   DecodeArgs a{};
   a.out = out;
   a.query = query;
@@ -871,10 +818,12 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
   a.max_parts = plan.max_parts;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.block_size = block_size;
-  take_injection(&a.skip_tile, &a.wait_limit_ns);
+  take_injection(&a.skip_tile, &a.wait_limit_ns);  // (this kernel has no wait that can run out)
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int qd = q_dtype == PA_F16 ? kF16 : kBF16;
-  st = cuda_status(decode_mxfp4(a, maps, qd, head_dim, cs), "decode_mxfp4");
+  const pa_status st = cuda_status(
+      decode_mxfp4(a, {key_cache, value_cache, k_scales, v_scales}, qd, head_dim, cs),
+      "decode_mxfp4");
   if (st != PA_OK || plan.max_parts <= 1) return st;
   return cuda_status(launch_reduce(a, qd, head_dim, cs), "decode_mxfp4 combine");
 }

@@ -87,8 +87,8 @@ cudaError_t decode_fp8_tc(const DecodeArgs& a, const CUtensorMap& kmap, const CU
 // kv-heads per CTA of that kernel (its TMA boxes span as many heads).
 int decode_fp8_tc_heads_per_cta(int num_kv_heads, int group);
 
-// Decode over an MXFP4 cache; maps: K codes, V codes, K scales, V scales.
-cudaError_t decode_mxfp4(const DecodeArgs& a, const CUtensorMap (&maps)[4], int q_dtype,
+// Decode over an MXFP4 cache; planes: K codes, V codes, K scales, V scales.
+cudaError_t decode_mxfp4(const DecodeArgs& a, const uint8_t* const (&planes)[4], int q_dtype,
                          int head_dim, cudaStream_t stream);
 
 // Rows of 16-bit values into / out of an MXFP4 cache, by slot.

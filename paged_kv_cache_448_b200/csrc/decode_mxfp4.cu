@@ -4,8 +4,12 @@
 // over the context, K_t and V_t being code * 2^(b - 127) per 32-element block
 // (mxfp4.cuh). One CTA per (kv-head, sequence, partition); each warp owns
 // every NW-th step of 32 tokens and streams it through its own ring of
-// shared-memory stages (per cache block one TMA box of K codes, K scales, V
-// codes, V scales; 136 bytes a token and kv-head at head_dim 128).
+// shared-memory stages with 16-byte asynchronous copies (136 bytes a token and
+// kv-head at head_dim 128; one block and head is 1 KB of codes). Plain copies
+// and not TMA boxes: a step has eight boxes (K and V, codes and scales, two
+// blocks), whose issue took an eighth of the instructions, and a launch
+// encodes no tensor maps. A warp waits for its own copies alone, which always
+// complete: nothing here can run out of time.
 //
 // Arithmetic on a step, per warp, on mma.sync m16n8k16 (f16 in, fp32
 // accumulators) with the tokens (S) or the dims (O) on M and the group's
@@ -57,15 +61,12 @@ struct MxCfg {
   static constexpr int RB = D / 2;                    // code bytes of a row
   static constexpr int SB = D / 32;                   // scale bytes of a row = blocks
   static constexpr int CODES = kStep * RB;            // K (or V) codes of a step
-  static constexpr int SCALES = 256;  // K (or V) scales of a step: a 128-byte slot per box
-  static constexpr int SWZ = RB == 64 ? 0x30 : 0x10;  // TMA 64-byte / 32-byte swizzle
-  static constexpr int R = 3;                         // stages of a warp's ring
-  static constexpr int STAGE = 2 * CODES;             // K codes, V codes
-  static constexpr int SSTAGE = 2 * SCALES;           // K scales, V scales
-  static constexpr int OFF_S = NW * R * STAGE;
-  static constexpr int OFF_BAR = OFF_S + NW * R * SSTAGE;
-  static constexpr int OFF_IDS = OFF_BAR + 8 * NW * R;
-  static_assert(NW * 8 * (D + 1) * 4 + NW * 16 * 4 <= NW * R * STAGE, "merge buffer fits");
+  static constexpr int SCALES = kStep * SB;           // K (or V) scales of a step
+  static constexpr int SWZ = RB == 64 ? 0x30 : 0x10;  // 16-byte chunks of a row XOR its number / 2 (4)
+  static constexpr int R = 2;                         // stages of a warp's ring
+  static constexpr int STAGE = 2 * CODES + 2 * SCALES;  // K codes, V codes, K scales, V scales
+  static constexpr int OFF_IDS = NW * R * STAGE;
+  static_assert(NW * 8 * (D + 1) * 4 + NW * 16 * 4 <= OFF_IDS, "merge buffer fits");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -119,14 +120,21 @@ __device__ __forceinline__ uint32_t f16_pow2(uint32_t x, int r) {
   return x * 0x400u + static_cast<uint32_t>(15 - r) * 0x04000400u;
 }
 
-// f16 of 2^(v - r) for the halves v of x with max(r - below, 1) <= v <= r + 7,
-// 0 for the others (a scale byte of 0 reads as 0).
-__device__ __forceinline__ uint32_t weights(uint32_t x, int r, int below) {
-  const int lo = max(r - below, 1);
-  const uint32_t in = halves_within(x, lo, r + 7);
+// f16 of 2^(v - r) for the halves v of x with max(r - 14, 1) <= v <= r, 0 for the others.
+__device__ __forceinline__ uint32_t band_pow2(uint32_t x, int r) {
+  const uint32_t in = halves_within(x, max(r - 14, 1), r);
   const uint32_t keep = ((in & 0xffffu) ? 0x0000ffffu : 0u) | ((in >> 16) ? 0xffff0000u : 0u);
   // the halves left out take the value r first: no carry into the other half
-  return f16_pow2(in | (static_cast<uint32_t>(max(r, 0)) * 0x10001u & ~keep), max(r, 0)) & keep;
+  return f16_pow2(in | (static_cast<uint32_t>(r) * 0x10001u & ~keep), r) & keep;
+}
+
+// The halves v of x with max(r - 8, 1) <= v <= r + 7 as they are, the others
+// such that f16_pow2 gives 0 (a scale byte of 0 reads as 0).
+__device__ __forceinline__ uint32_t window_only(uint32_t x, int r) {
+  const int a = static_cast<int>(x & 0xffffu), b = static_cast<int>(x >> 16);
+  const int lo = max(r - 8, 1), hi = r + 7;
+  return static_cast<uint32_t>(b >= lo && b <= hi ? b : r - 15) * 0x10000u +
+         static_cast<uint32_t>(a >= lo && a <= hi ? a : r - 15);
 }
 
 // m's bits of x, the others of y.
@@ -180,25 +188,16 @@ __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return (~w - 0x01010101u) & w & 0x80808080u;
 }
 
-// The TMA box of one block: its rows of one kv-head (codes), or the scales of
-// those rows. Coordinates: byte within the row, row (or byte) within the
-// block, block.
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, int32_t c2, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar)),
-      "l"(policy)
-      : "memory");
+// 16 bytes global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The attention state of one warp: query heads 2c and 2c+1 of lane (g, c),
@@ -279,12 +278,12 @@ struct MxState {
   }
   static __device__ __forceinline__ int byte_of(uint32_t w, int b) { return (w >> (8 * b)) & 255; }
 
-  // One step: kStep rows of codes at kc / vc (swizzled), scales at ks / vs
-  // (those of rows 16 and up `half` bytes further); rows from `valid` on are
-  // not of the context and may hold anything.
-  template <int SWZ>
+  // One step: kStep rows of codes at kc / vc (swizzled), scales at ks / vs;
+  // if PARTIAL, rows from `valid` on are not of the context and may hold
+  // anything (a copy of its own: masks would cost every step a tenth).
+  template <int SWZ, bool PARTIAL>
   __device__ __forceinline__ void step(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
-                                       const uint8_t* vs, int half, int valid, int lane) {
+                                       const uint8_t* vs, int valid, int lane) {
     constexpr int SB = NB;
     constexpr unsigned FULL = 0xffffffffu;
     const int g = lane >> 2, c = lane & 3;
@@ -298,8 +297,8 @@ struct MxState {
       load_codes<D, SWZ, false>(kc, u, lane, r);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        kw[u][i] = scale_word(ks + u * half + (8 * i + g) * SB);
-        if (valid < kStep && 16 * u + 8 * i + g >= valid) kw[u][i] = 0u;
+        kw[u][i] = scale_word(ks + (16 * u + 8 * i + g) * SB);
+        if (PARTIAL && 16 * u + 8 * i + g >= valid) kw[u][i] = 0u;
         ff |= has_ff(kw[u][i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) x[u][i][j] = 0.f;
@@ -327,7 +326,7 @@ struct MxState {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* p = vs + u * half + (8 * i + 2 * c) * SB;
+        const uint8_t* p = vs + (16 * u + 8 * i + 2 * c) * SB;
         if constexpr (NB == 4) {
           const uint2 t = *reinterpret_cast<const uint2*>(p);
           vw[u][i][0] = t.x;
@@ -338,7 +337,7 @@ struct MxState {
           vw[u][i][1] = t >> 16;
         }
       }
-    if (valid < kStep) {  // the last step of a unit
+    if constexpr (PARTIAL) {  // the last step of a unit
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -373,11 +372,11 @@ struct MxState {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float t = x[u][i][j] * qs[j];
-          if (valid < kStep && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
+          if (PARTIAL && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
           x[u][i][j] = t;
           mx[j] = fmaxf(mx[j], t);
         }
-    if (valid < kStep) {  // rows that are not of the context: a scale within the window
+    if constexpr (PARTIAL) {  // rows that are not of the context: a scale within the window
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -411,6 +410,15 @@ struct MxState {
         const __half2 h = __floats2half2_rn(p0, p1);
         p[u][i] = movm_trans(*reinterpret_cast<const uint32_t*>(&h));
       }
+    if (wide) {  // the bands below the window; those tokens weigh nothing after this
+      bands<SWZ>(vc, p, ex, lane);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) ex[u][i][b] = window_only(ex[u][i][b], ref[b]);
+    }
     // ---- O += V^T (P 2^(bV - r))
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -418,11 +426,7 @@ struct MxState {
       load_codes<D, SWZ, true>(vc, u, lane, r);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint32_t f0 = f16_pow2(ex[u][0][b], ref[b]), f1 = f16_pow2(ex[u][1][b], ref[b]);
-        if (wide) {  // tokens outside the window weigh nothing here
-          f0 = weights(ex[u][0][b], ref[b], 8);
-          f1 = weights(ex[u][1][b], ref[b], 8);
-        }
+        const uint32_t f0 = f16_pow2(ex[u][0][b], ref[b]), f1 = f16_pow2(ex[u][1][b], ref[b]);
         uint32_t h[2][4];
         v_pairs(r[0][b], h[0]);
         v_pairs(r[1][b], h[1]);
@@ -431,7 +435,6 @@ struct MxState {
         mma16816(o[b][1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
       }
     }
-    if (wide) bands<SWZ>(vc, p, ex, lane);
   }
 
   // Nonzero if some V scale of the step (exponents of ex) is not within
@@ -485,8 +488,8 @@ struct MxState {
           v_pairs(r[1], h[1]);
           const uint32_t e0 = u ? ex[1][0][b] : ex[0][0][b], e1 = u ? ex[1][1][b] : ex[0][1][b];
           const uint32_t p0 = u ? p[1][0] : p[0][0], p1 = u ? p[1][1] : p[0][1];
-          const uint32_t b0 = hmul2u(p0, weights(halves_within(e0, 1, t), t, 14));
-          const uint32_t b1 = hmul2u(p1, weights(halves_within(e1, 1, t), t, 14));
+          const uint32_t b0 = hmul2u(p0, band_pow2(e0, t));
+          const uint32_t b1 = hmul2u(p1, band_pow2(e1, t));
           mma16816(add[0], h[0][0], h[0][1], h[1][0], h[1][1], b0, b1);
           mma16816(add[1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
         }
@@ -673,15 +676,15 @@ struct MxStateN {
     low = true;
   }
 
-  template <int SWZ>
+  template <int SWZ, bool PARTIAL>
   __device__ __forceinline__ void step(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
-                                       const uint8_t* vs, int half, int valid, int lane) {
+                                       const uint8_t* vs, int valid, int lane) {
     constexpr int SB = NB;
     constexpr unsigned FULL = 0xffffffffu;
     const int g = lane >> 2, c = lane & 3;
     // ---- logits: x[u][i] = token 16 u + 8 i + g, the head of columns 2c, 2c+1
     float x[2][2];
-    uint32_t ff[2][2], any_ff = 0u;
+    float fs[2][2], top = 0.f;  // larger scale of the two columns: infinity for a byte of 255
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t r[2][NB];
@@ -698,13 +701,13 @@ struct MxStateN {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         // the scale bytes of this lane's two columns
-        uint32_t y = *reinterpret_cast<const uint16_t*>(ks + u * half + (8 * i + g) * SB +
+        uint32_t y = *reinterpret_cast<const uint16_t*>(ks + (16 * u + 8 * i + g) * SB +
                                                         (2 * c) % NB);
-        if (valid < kStep && 16 * u + 8 * i + g >= valid) y = 0u;
-        ff[u][i] = has_ff(y);
-        any_ff |= ff[u][i];
+        if (PARTIAL && 16 * u + 8 * i + g >= valid) y = 0u;
         const float f0 = __uint_as_float((y << 23) & 0x7f800000u);
         const float f1 = __uint_as_float((y << 15) & 0x7f800000u);
+        fs[u][i] = fmaxf(f0, f1);
+        top = fmaxf(top, fs[u][i]);
         x[u][i] = fmaf(f0, s[2 * i], f1 * s[2 * i + 1]);
         if constexpr (NB == 4) x[u][i] += __shfl_xor_sync(FULL, x[u][i], 1);
       }
@@ -715,7 +718,7 @@ struct MxStateN {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* p = vs + u * half + (8 * i + 2 * c) * SB;
+        const uint8_t* p = vs + (16 * u + 8 * i + 2 * c) * SB;
         const uint32_t b = g % NB;
         if constexpr (NB == 4) {
           const uint2 t = *reinterpret_cast<const uint2*>(p);
@@ -731,11 +734,11 @@ struct MxStateN {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float t = x[u][i] * qs;
-        if (valid < kStep && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
+        if (PARTIAL && 16 * u + 8 * i + g >= valid) t = -CUDART_INF_F;
         x[u][i] = t;
         mx = fmaxf(mx, t);
       }
-    if (valid < kStep) {  // rows that are not of the context: a scale within the window
+    if constexpr (PARTIAL) {  // rows that are not of the context: a scale within the window
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -745,15 +748,15 @@ struct MxStateN {
           ex[u][i] = (ex[u][i] & keep) | (static_cast<uint32_t>(max(own, 1)) * 0x10001u & ~keep);
         }
     }
-    const bool lift = mx > m + 8.f || outside(ex) || any_ff;
+    const bool lift = mx > m + 8.f || outside(ex) || top == CUDART_INF_F;
     bool wide = low;  // (the same in every lane)
     if (__any_sync(FULL, lift)) {
-      update(x, mx, ff, ex, lane);
+      update(x, mx, fs, ex, lane);
       wide = low || __any_sync(FULL, outside(ex));
     }
     // ---- probabilities, their sum, and P as B operand (tokens x columns)
     const float mu = m == -CUDART_INF_F ? 0.f : m;
-    uint32_t p[2][2], pb[2][2];
+    uint32_t p[2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -762,24 +765,30 @@ struct MxStateN {
         l += e;
         const __half2 h = __floats2half2_rn(e, e);
         p[u][i] = movm_trans(*reinterpret_cast<const uint32_t*>(&h));
-        const uint32_t f = wide ? weights(ex[u][i], own, 8) : f16_pow2(ex[u][i], own);
-        pb[u][i] = hmul2u(p[u][i], f);
       }
+    if (wide) {  // the bands below the window; those tokens weigh nothing after this
+      bands<SWZ>(vc, p, ex, lane);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ex[u][i] = window_only(ex[u][i], own);
+    }
     // ---- O += V^T (P 2^(bV - r))
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t r[2][NB];
       load_codes<D, SWZ, true>(vc, u, lane, r);
+      const uint32_t b0 = hmul2u(p[u][0], f16_pow2(ex[u][0], own));
+      const uint32_t b1 = hmul2u(p[u][1], f16_pow2(ex[u][1], own));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t h[2][4];
         v_pairs(r[0][b], h[0]);
         v_pairs(r[1][b], h[1]);
-        mma16816(o[b][0], h[0][0], h[0][1], h[1][0], h[1][1], pb[u][0], pb[u][1]);
-        mma16816(o[b][1], h[0][2], h[0][3], h[1][2], h[1][3], pb[u][0], pb[u][1]);
+        mma16816(o[b][0], h[0][0], h[0][1], h[1][0], h[1][1], b0, b1);
+        mma16816(o[b][1], h[0][2], h[0][3], h[1][2], h[1][3], b0, b1);
       }
     }
-    if (wide) bands<SWZ>(vc, p, ex, lane);
   }
 
   // Nonzero if a V scale of the step is not within [r_b - 8, r_b + 7].
@@ -819,8 +828,8 @@ struct MxStateN {
       for (int u = 0; u < 2; ++u) {
         uint32_t r[2][NB];
         load_codes<D, SWZ, true>(vc, u, lane, r);
-        const uint32_t b0 = t > 0 ? hmul2u(p[u][0], weights(halves_within(ex[u][0], 1, t), t, 14)) : 0u;
-        const uint32_t b1 = t > 0 ? hmul2u(p[u][1], weights(halves_within(ex[u][1], 1, t), t, 14)) : 0u;
+        const uint32_t b0 = t > 0 ? hmul2u(p[u][0], band_pow2(ex[u][0], t)) : 0u;
+        const uint32_t b1 = t > 0 ? hmul2u(p[u][1], band_pow2(ex[u][1], t)) : 0u;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t h[2][4];
@@ -840,7 +849,7 @@ struct MxStateN {
   }
 
   // MxState::update: maxima and references move, NaN scales are looked at.
-  __device__ __forceinline__ void update(float (&x)[2][2], float mx, const uint32_t (&ff)[2][2],
+  __device__ __forceinline__ void update(float (&x)[2][2], float mx, const float (&fs)[2][2],
                                          uint32_t (&ex)[2][2], int lane) {
     constexpr unsigned FULL = 0xffffffffu;
     const int g = lane >> 2;
@@ -849,9 +858,9 @@ struct MxStateN {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint32_t bad = ff[u][i];
-        if constexpr (NB == 4) bad |= __shfl_xor_sync(FULL, bad, 1);
-        if (bad) x[u][i] = CUDART_NAN_F;
+        float t = fs[u][i];
+        if constexpr (NB == 4) t = fmaxf(t, __shfl_xor_sync(FULL, t, 1));
+        if (t == CUDART_INF_F) x[u][i] = CUDART_NAN_F;
       }
 #pragma unroll
     for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
@@ -929,36 +938,22 @@ struct MxStateN {
   }
 };
 
+// The planes of the cache: K codes, V codes, K scales, V scales.
+struct MxPlanes {
+  const uint8_t* p[4];
+};
+
 template <class QF, int D, int NW, bool BLOCKS_ON_N>
 __global__ void __launch_bounds__(NW * 32, BLOCKS_ON_N ? 4 : 3)
-    paged_decode_mxfp4_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
-                              const __grid_constant__ CUtensorMap vmap,
-                              const __grid_constant__ CUtensorMap ksmap,
-                              const __grid_constant__ CUtensorMap vsmap) {
+    paged_decode_mxfp4_kernel(const DecodeArgs a, const MxPlanes planes) {
   using C = MxCfg<D, NW>;
-  constexpr int R = C::R;
-  constexpr unsigned FULL = 0xffffffffu;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  constexpr int R = C::R, RB = C::RB, SB = C::SB;
+  extern __shared__ __align__(128) uint8_t smem[];
   int32_t* ids = reinterpret_cast<int32_t*>(smem + C::OFF_IDS);
-  __shared__ int aborted;
 
   const int kvh = blockIdx.x, s = blockIdx.y, part = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.num_heads / a.num_kv_heads;
-  if (lane == 0) {
-    for (int r = 0; r < R; ++r) mbar_init(&bars[warp * R + r], 1);
-    fence_mbar_init();
-  }
-  if (threadIdx.x == 0) {
-    aborted = 0;
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-    prefetch_tensormap(&ksmap);
-    prefetch_tensormap(&vsmap);
-  }
   // everything below reads what earlier kernels of the stream wrote
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -982,88 +977,77 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS_ON_N ? 4 : 3)
     int32_t id = table[b_begin + i];
     if (id < 0 || id >= a.num_blocks) {
       report(a.err, kErrBadBlockId);
-      id = -1;  // a box outside the pool: zero codes and scales
+      id = -1;  // zero codes and scales
     }
     ids[i] = id;
   }
   __syncthreads();
 
   const int my_count = nsteps > warp ? (nsteps - warp + NW - 1) / NW : 0;
-  uint8_t* my_codes = smem + warp * R * C::STAGE;
-  uint8_t* my_scales = smem + C::OFF_S + warp * R * C::SSTAGE;
-  uint64_t* my_bars = bars + warp * R;
-  const uint64_t policy = l2_policy_evict_first();
-
-  const int half = bs == 16 ? 128 : 16 * C::SB;  // from the scales of row 15 to those of row 16
-  auto issue = [&](int k) {  // k-th step of this warp
-    const int t0 = (warp + k * NW) * kStep;
-    const int stage = k % R;
-    const int blk0 = t0 / bs, n = min(nlocal - blk0, kStep / bs);
-    mbar_arrive_expect_tx(&my_bars[stage], static_cast<uint32_t>(n * bs * 2 * (C::RB + C::SB)));
-    uint8_t* codes = my_codes + stage * C::STAGE;
-    uint8_t* scales = my_scales + stage * C::SSTAGE;
-    for (int j = 0; j < n; ++j) {
-      // a failure-detection test leaves out the block that holds its tile
-      const int tile0 = (t0 + j * bs) / kTileRows;
-      if (a.skip_tile >= tile0 && a.skip_tile < tile0 + bs / kTileRows &&
-          skip_for_test(a.skip_tile, a.skip_tile))
-        continue;
-      const int32_t id = ids[blk0 + j];
-      tma_load_3d(codes + j * bs * C::RB, &kmap, &my_bars[stage], 0, kvh * bs, id, policy);
-      tma_load_2d(scales + j * 128, &ksmap, &my_bars[stage], kvh * bs * C::SB, id, policy);
-      tma_load_3d(codes + C::CODES + j * bs * C::RB, &vmap, &my_bars[stage], 0, kvh * bs, id,
-                  policy);
-      tma_load_2d(scales + C::SCALES + j * 128, &vsmap, &my_bars[stage], kvh * bs * C::SB, id,
-                  policy);
+  uint8_t* ring = smem + warp * R * C::STAGE;
+  // Copies of this warp's k-th step (one group of asynchronous copies each,
+  // empty past the last). Rows 16 u .. of a step are 16 rows of one block:
+  // contiguous codes and scales, of which lane l copies the 16 bytes from 16 l.
+  const int32_t cstride = a.num_kv_heads * bs * RB, sstride = a.num_kv_heads * bs * SB;
+  const uint32_t ring0 = smem_addr(ring);
+  const int lane16 = lane * 16, swizzled = lane16 ^ ((lane16 >> 3) & C::SWZ);
+  // scale copies: SL lanes for K, as many for V, half of them for each 16 rows
+  constexpr int SL = C::SCALES / 16;
+  const int sv = lane / SL, sc = lane % SL, su = sc / (SL / 2);
+  const uint8_t* scale_plane = (sv ? planes.p[3] : planes.p[2]) +
+                               static_cast<int64_t>(kvh) * bs * SB + sc % (SL / 2) * 16;
+  const uint8_t* k_plane = planes.p[0] + static_cast<int64_t>(kvh) * bs * RB + lane16;
+  const uint8_t* v_plane = planes.p[1] + static_cast<int64_t>(kvh) * bs * RB + lane16;
+  auto issue = [&](int k) {
+    if (k < my_count) {
+      const int t0 = (warp + k * NW) * kStep;
+      const uint32_t dst = ring0 + (k % R) * C::STAGE;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int blk = bs == 16 ? t0 / 16 + u : t0 / 32, row = bs == 16 ? 0 : 16 * u;
+        if (blk >= nlocal) break;
+        const int32_t id = ids[blk];
+        const int32_t b = max(id, 0);
+        const uint8_t* k_src = k_plane + static_cast<int64_t>(b) * cstride + row * RB;
+        const uint8_t* v_src = v_plane + static_cast<int64_t>(b) * cstride + row * RB;
+#pragma unroll
+        for (int i = 0; i < RB / 32; ++i) {  // 512 bytes each
+          copy16(dst + (u * (RB / 32) + i) * 512 + swizzled, k_src + i * 512, id >= 0);
+          copy16(dst + C::CODES + (u * (RB / 32) + i) * 512 + swizzled, v_src + i * 512,
+                 id >= 0);
+        }
+        if (su == u && sv < 2)
+          copy16(dst + 2 * C::CODES + lane16, scale_plane + static_cast<int64_t>(b) * sstride + row * SB, id >= 0);
+      }
     }
+    copy_commit();
   };
-  if (lane == 0) {
-    for (int k = 0; k < min(R, my_count); ++k) issue(k);
-  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) issue(k);
 
   typename std::conditional<BLOCKS_ON_N, MxStateN<QF, D>, MxState<QF, D>>::type st;
   const int64_t row0 = static_cast<int64_t>(s) * a.num_heads + kvh * group;
   st.init(a, static_cast<const uint8_t*>(a.query) + row0 * D * 2, group, lane);
-  int k = 0;
-  for (; k < my_count; ++k) {
-    const int stage = k % R;
-    if (!__all_sync(FULL, mbar_wait(&my_bars[stage], (k / R) & 1, a.wait_limit_ns, &aborted)))
-      break;
-    const uint8_t* codes = my_codes + stage * C::STAGE;
-    const uint8_t* scales = my_scales + stage * C::SSTAGE;
-    st.template step<C::SWZ>(codes, codes + C::CODES, scales, scales + C::SCALES, half,
-                             min(kStep, tokens - (warp + k * NW) * kStep), lane);
+  for (int k = 0; k < my_count; ++k) {
+    copy_wait<R - 1>();
+    __syncwarp();  // every lane's copies of the step
+    const uint8_t* stage = ring + (k % R) * C::STAGE;
+    const uint8_t* scales = stage + 2 * C::CODES;
+    const int valid = tokens - (warp + k * NW) * kStep;
+    if (valid >= kStep)
+      st.template step<C::SWZ, false>(stage, stage + C::CODES, scales, scales + C::SCALES, kStep,
+                                      lane);
+    else
+      st.template step<C::SWZ, true>(stage, stage + C::CODES, scales, scales + C::SCALES, valid,
+                                     lane);
     __syncwarp();
-    if (lane == 0 && k + R < my_count) issue(k + R);
+    issue(k + R);
   }
-  if (k < my_count) {
-    // a wait gave up (never expected): record it, let this warp's loads in
-    // flight land (bounded again), and stop the CTA after the barrier
-    if (lane == 0) {
-      record_failure(a.diag, kSiteTile, blockIdx.x, blockIdx.y, blockIdx.z, warp, k, my_count, 0);
-      aborted = 1;
-    }
-    for (int kk = k; kk < min(k + R, my_count); ++kk)
-      mbar_wait(&my_bars[kk % R], (kk / R) & 1, a.wait_limit_ns);
-  }
+  copy_wait<0>();
 
-  // merge the warps through shared memory (every issued load has landed)
+  // merge the warps through shared memory (every copy has landed)
   __syncthreads();
   const bool single = parts == 1;
-  if (aborted) {
-    // the unit's result is lost: zeros, or an empty partial that the combine
-    // kernel gives no weight, never stale data
-    if (threadIdx.x == 0) report(a.err, kErrWaitTimeout);
-    for (int idx = threadIdx.x; idx < group * D; idx += NW * 32) {
-      const int h = idx / D, d = idx % D;
-      if (single) {
-        store_out(QF{}, a.out, (row0 + h) * D + d, 0.f);
-      } else if (d == 0) {
-        a.ws_ml[(row0 + h) * a.max_parts + part] = make_float2(-CUDART_INF_F, 0.f);
-      }
-    }
-    return;
-  }
   float* mbuf = reinterpret_cast<float*>(smem);  // [NW][8][2]: m, l
   float* obuf = mbuf + NW * 16;                  // [NW][8][D]
   st.finish(mbuf + warp * 16, obuf + warp * 8 * D, group, lane);
@@ -1097,27 +1081,28 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS_ON_N ? 4 : 3)
 }
 
 template <class QF, int D, int NW, bool BLOCKS_ON_N>
-cudaError_t launch_mx(const DecodeArgs& a, const CUtensorMap (&maps)[4], cudaStream_t stream) {
+cudaError_t launch_mx(const DecodeArgs& a, const MxPlanes& planes, cudaStream_t stream) {
   using C = MxCfg<D, NW>;
   if (a.partition_blocks > kMaxUnitBlocks || kStep % a.block_size != 0)
     return cudaErrorNotSupported;
-  const size_t smem = 1024 + C::OFF_IDS + 4 * static_cast<size_t>(a.partition_blocks);
+  const size_t smem = C::OFF_IDS + 4 * static_cast<size_t>(a.partition_blocks);
   auto kern = paged_decode_mxfp4_kernel<QF, D, NW, BLOCKS_ON_N>;
   cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.num_kv_heads, a.num_seqs, a.max_parts), NW * 32, smem, stream, a,
-                    maps[0], maps[1], maps[2], maps[3]);
+                    planes);
 }
 
 }  // namespace
 
-cudaError_t decode_mxfp4(const DecodeArgs& a, const CUtensorMap (&maps)[4], int q_dtype,
+cudaError_t decode_mxfp4(const DecodeArgs& a, const uint8_t* const (&planes)[4], int q_dtype,
                          int head_dim, cudaStream_t stream) {
+  const MxPlanes pl{{planes[0], planes[1], planes[2], planes[3]}};
   const int group = a.num_heads / a.num_kv_heads;
   const bool n = group * (head_dim / 32) <= 8;
 #define PAGED_MX(QT, QF, d)                                                     \
   if (q_dtype == QT && head_dim == d)                                          \
-    return n ? launch_mx<QF, d, 4, true>(a, maps, stream) : launch_mx<QF, d, 4, false>(a, maps, stream);
+    return n ? launch_mx<QF, d, 4, true>(a, pl, stream) : launch_mx<QF, d, 4, false>(a, pl, stream);
   PAGED_MX(kF16, F16, 64)
   PAGED_MX(kF16, F16, 128)
   PAGED_MX(kBF16, BF16, 64)
