@@ -694,8 +694,7 @@ pa_status check_mxfp4_rows(const char* what, const void* key, const void* value,
                 block_size);
   if (kv_dtype != PA_F16 && kv_dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "%s: rows must be f16 or bf16", what);
-  if (static_cast<int64_t>(num_tokens) * hkv * (head_dim / 8) / 256 >= INT32_MAX)
-    return fail(PA_ERR_UNSUPPORTED, "%s: too many rows for one launch", what);
+  if (hkv > 65536) return fail(PA_ERR_UNSUPPORTED, "%s: more than 65536 kv-heads", what);
   if (num_tokens == 0) return PA_OK;
   if (!key || !value || !kc || !vc || !ks || !vs || !slots)
     return fail(PA_ERR_INVALID_ARG, "%s: null pointer", what);

@@ -143,7 +143,7 @@ def test_rows_refusals(name):
     for arg in ("key", "value", "kc", "vc", "ks", "vs", "slots"):
         assert call(**{arg: None}) == BAD, arg
         assert call(**{arg: P + 2}) == BAD, arg
-    assert call(T=2 ** 31 - 1, Hkv=64) == UNSUP
+    assert call(Hkv=65537) == UNSUP
 
 
 def test_decode_refusals():
