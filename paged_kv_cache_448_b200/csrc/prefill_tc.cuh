@@ -186,7 +186,7 @@ __device__ __forceinline__ float2 unpack_q(uint32_t w) {
   return __half22float2(h);
 }
 
-// Largest magnitude of eight bf16 values, and the values times 2^e as f16.
+// Largest magnitude of eight bf16 values, and the values times s as f16.
 __device__ __forceinline__ float chunk_max(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float m = 0.f;
@@ -197,13 +197,13 @@ __device__ __forceinline__ float chunk_max(const uint4& v) {
   }
   return m;
 }
-__device__ __forceinline__ uint4 scaled_f16(const uint4& v, int e) {
+__device__ __forceinline__ uint4 scaled_f16(const uint4& v, float s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = unpack_q<BF16>(w[j]);
-    o[j] = pack2<false>(ldexpf(f.x, e), ldexpf(f.y, e));
+    o[j] = pack2<false>(f.x * s, f.y * s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -413,28 +413,45 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     const int kv_end = min(ctx, tend * TR);
     const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
     const int bs_log = a.block_size == 32 ? 5 : 4;
-    int top[2] = {0, 0};
-    for (int t = tbase * TR + tid; t < kv_end; t += C::THREADS) {
-      const int32_t id = table[t >> bs_log];
-      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.num_blocks)) continue;
-      const int64_t row = (static_cast<int64_t>(id) * a.num_kv_heads + kvh) * a.block_size +
-                          (t & (a.block_size - 1));
+    // 16 bytes of scales a thread and load (VT tokens of one block), several
+    // loads of block ids, then of scales, in flight
+    constexpr int NB = D / 32, VT = 16 / NB, BATCH = 3;
+    uint32_t top[2] = {0u, 0u};
+    for (int t0 = tbase * TR + tid * VT; t0 < kv_end; t0 += BATCH * C::THREADS * VT) {
+      int32_t id[BATCH];
+      uint4 w[BATCH][2];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint8_t* p = cache.scales[v] + row * (D / 32);
-        const uint32_t w = D == 128 ? __ldcg(reinterpret_cast<const uint32_t*>(p))
-                                    : __ldcg(reinterpret_cast<const uint16_t*>(p));
+      for (int j = 0; j < BATCH; ++j)
+        id[j] = table[min(t0 + j * C::THREADS * VT, kv_end - 1) >> bs_log];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int b = (w >> (8 * i)) & 255;
-          if (b != kMxNan) top[v] = max(top[v], b);
+      for (int j = 0; j < BATCH; ++j) {
+        const bool known = static_cast<uint32_t>(id[j]) < static_cast<uint32_t>(a.num_blocks);
+        const int t = t0 + j * C::THREADS * VT;
+        const int64_t row = (static_cast<int64_t>(known ? id[j] : 0) * a.num_kv_heads + kvh) *
+                                a.block_size + (t & (a.block_size - 1));
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          w[j][v] = __ldcg(reinterpret_cast<const uint4*>(cache.scales[v] + row * NB));
+        if (!known) id[j] = -1;
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int rows = id[j] < 0 ? 0 : kv_end - (t0 + j * C::THREADS * VT);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t x[4] = {w[j][v].x, w[j][v].y, w[j][v].z, w[j][v].w};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t b = (x[i / 4] >> (8 * (i % 4))) & 255u;
+            if (i / NB < rows && b != kMxNan) top[v] = max(top[v], b);
+          }
         }
       }
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       top[v] = __reduce_max_sync(0xffffffffu, top[v]);
-      if (lane == 0) ref_part[v][warp] = top[v];
+      if (lane == 0) ref_part[v][warp] = static_cast<int>(top[v]);
     }
   }
   __syncthreads();  // barrier initialisation visible to every thread
@@ -454,34 +471,46 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     const int g = tid / kTcRows, rr = tid % kTcRows;
     const uint4* q4 = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.query) +
                                                      row_off * 2);
-    if constexpr (MX) {
-      int qe = 0;
-      if constexpr (C::OBF) {
-        float mq = 0.f;
-        if (valid) {
+    if constexpr (!FP8) {
+      // a warp loads its 32 rows some whole rows at a time (D / 8 lanes each):
+      // with a row per thread every load touched 32 lines, and the prologue
+      // took a fifth of a unit's time (measured: 8 100 of 61 500 cycles,
+      // 512-token chunks)
+      constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of one load
+      constexpr int LOADS = 32 / RPL, BATCH = 8;
+      const int c = lane % LPR;
+      int qe = 0;  // MXFP4, bf16 query: power of two of this thread's own row
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) mq = fmaxf(mq, chunk_max(q4[c]));
+      for (int j0 = 0; j0 < LOADS; j0 += BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int r = warp * 32 + (j0 + j) * RPL + lane / LPR, u = dup ? r & 63 : r;
+          v[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (u / G < ntok)
+            v[j] = reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(a.query) +
+                (static_cast<int64_t>(q0 + tok0 + u / G) * a.num_heads + kvh * G + u % G) * D *
+                    2)[c];
         }
-        if (mq > 0.f && isfinite(mq)) qe = -max(ilogbf(mq), -126);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          if constexpr (MX && C::OBF) {
+            float mq = chunk_max(v[j]);
+#pragma unroll
+            for (int d = 1; d < LPR; d *= 2) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, d));
+            const int field = static_cast<int>(__float_as_uint(mq) >> 23);
+            const int e = mq > 0.f && field < 255 ? min(max(127 - field, -126), 126) : 0;
+            v[j] = scaled_f16(v[j], __uint_as_float(static_cast<uint32_t>(e + 127) << 23));
+            const int er = __shfl_sync(0xffffffffu, e, lane % RPL * LPR);
+            if (lane / RPL == j0 + j) qe = er;
+          }
+          const int rg = (warp % 4) * 32 + (j0 + j) * RPL + lane / LPR;
+          *reinterpret_cast<uint4*>(sq(g) + c / 8 * C::QPART + sw128(rg, c % 8)) = v[j];
+        }
       }
       // (the exponents together: each alone may leave fp32's range)
-      qscale = ldexpf(qscale, ref_k - kMxTrueRef - qe);
-#pragma unroll
-      for (int sg = 0; sg < NSEG; ++sg)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (C::OBF) v = scaled_f16(v, qe);
-          *reinterpret_cast<uint4*>(sq(g) + sg * C::QPART + sw128(rr, c)) = v;
-        }
-    } else if constexpr (!FP8) {
-#pragma unroll
-      for (int sg = 0; sg < NSEG; ++sg)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = valid ? q4[sg * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(sq(g) + sg * C::QPART + sw128(rr, c)) = v;
-        }
+      if constexpr (MX && C::OBF) qscale = ldexpf(qscale, ref_k - kMxTrueRef - qe);
     } else {
       // row maximum, then q * 2^e = hi + lo (E4M3 each), 16 dims per 16-byte chunk
       float mq = 0.f;
