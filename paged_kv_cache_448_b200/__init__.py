@@ -235,110 +235,18 @@ def copy_blocks(src_key_cache, src_value_cache, dst_key_cache, dst_value_cache, 
 
 # ---------------------------------------------------------------- 4-bit cache
 
-# The calls below check what they are given in full and launch small kernels: the checks are
-# plain comparisons, and messages are put together only where one fails.
-
-class _Torch:
-    """What the checks use of torch, looked up once (torch is imported by whoever has tensors)."""
-
-    def __getattr__(self, name):
-        import torch
-        self.torch = torch
-        self.code = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
-        self.int32, self.uint8 = torch.int32, torch.uint8
-        self.current_device = torch.cuda.current_device
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.raw_stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        return self.__dict__[name]
+def _handle(stream):
+    """What the tensor calls take for a stream: its handle, or None for the current one of
+    the tensors' device."""
+    return None if stream is None else stream.cuda_stream
 
 
-_t = _Torch()
-
-
-def _launch(fn, dev, stream, *args) -> None:
-    """fn(*args, stream handle) with CUDA device `dev` current; without a stream, that
-    device's current one."""
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    handle = _t.raw_stream(dev) if stream is None else stream.cuda_stream
-    if dev == _t.current_device():
-        status = fn(*args, handle)
-    else:
-        with _t.torch.cuda.device(dev):
-            status = fn(*args, handle)
-    if status:
-        check(status)
-
-
-def _explain(tensors) -> None:
-    """Raise for the first of (name, tensor, dtypes, shape, device) that is not as it should
-    be; a None in a shape stands for any extent."""
-    for name, t, dtypes, shape, dev in tensors:
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
-        if t.dim() != len(shape) or any(w not in (None, n) for w, n in zip(shape, t.shape)):
-            raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on another device ({t.device})")
-
-
-def _check_mxfp4_planes(kc, vc, ks, vs, D, dev):
-    """(num_blocks, num_kv_heads, block_size) of an MXFP4 cache's planes."""
-    shape = kc.shape
-    if len(shape) != 4:
-        raise ValueError("key_cache must be [num_blocks, num_kv_heads, block_size, head_dim / 2]")
-    NB, Hkv, BS, _ = shape
-    u8 = _t.uint8
-    codes, scales = (NB, Hkv, BS, D // 2), (NB, Hkv, BS, D // 32)
-    if not (shape == codes and vc.shape == codes and ks.shape == scales and
-            vs.shape == scales and kc.dtype is u8 and vc.dtype is u8 and ks.dtype is u8 and
-            vs.dtype is u8 and kc.is_contiguous() and vc.is_contiguous() and
-            ks.is_contiguous() and vs.is_contiguous() and kc.get_device() == dev and
-            vc.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev):
-        _explain([("key_cache", kc, (u8,), codes, dev), ("value_cache", vc, (u8,), codes, dev),
-                  ("k_scales", ks, (u8,), scales, dev), ("v_scales", vs, (u8,), scales, dev)])
-    return NB, Hkv, BS
-
-
-def _check_pair(x, y, xname, yname):
-    """(pa_dtype, shape, device) of two 16-bit tensors [tokens, heads, head_dim] alike."""
-    shape, dt = x.shape, x.dtype
-    code, dev = _t.code.get(dt), x.get_device()
-    if not (code is not None and len(shape) == 3 and y.shape == shape and y.dtype is dt and
-            x.is_contiguous() and y.is_contiguous() and y.get_device() == dev):
-        _explain([(xname, x, tuple(_t.code), (None, None, None), dev),
-                  (yname, y, (dt,), tuple(shape), dev)])
-    return code, shape, dev
-
-
-def _check_ints(name, t, shape, dev):
-    if not (t.dtype is _t.int32 and t.shape == shape and t.is_contiguous() and
-            t.get_device() == dev):
-        _explain([(name, t, (_t.int32,), shape, dev)])
-
-
-def _check_table(name, t, rows, dev):
-    """(rows, max_blocks_per_seq) of a block table; rows None: any."""
-    shape = t.shape
-    if not (t.dtype is _t.int32 and len(shape) == 2 and rows in (None, shape[0]) and
-            t.is_contiguous() and t.get_device() == dev):
-        _explain([(name, t, (_t.int32,), (rows, None), dev)])
-    return shape
-
-
-def _check_workspace(t, dev):
-    if not (t.dtype is _t.uint8 and t.is_contiguous() and t.get_device() == dev):
-        _explain([("workspace", t, (_t.uint8,), (None,) * t.dim(), dev)])
-    return t.data_ptr(), t.numel()
-
-
-def _own_workspace(make, dev, stream):
+def _own_workspace(like, stream, make):
     """A workspace of one call's own, kept from reuse until `stream` has passed it."""
-    if dev < 0:
+    import torch
+    if not like.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    with _t.torch.cuda.device(dev):
+    with torch.cuda.device(like.device):
         ws = make()
     if stream is not None:
         ws.record_stream(stream)
@@ -355,23 +263,15 @@ def mxfp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):
                  for w in (head_dim // 2, head_dim // 2, head_dim // 32, head_dim // 32))
 
 
-def _mxfp4_rows(fn, key, value, kc, vc, ks, vs, slots, stream):
-    code, (T, Hkv, D), dev = _check_pair(key, value, "key", "value")
-    NB, heads, BS = _check_mxfp4_planes(kc, vc, ks, vs, D, dev)
-    if heads != Hkv:
-        raise ValueError(f"the cache has {heads} kv-heads, key {Hkv}")
-    _check_ints("slot_mapping", slots, (T,), dev)
-    _launch(fn, dev, stream, key.data_ptr(), value.data_ptr(), kc.data_ptr(), vc.data_ptr(),
-            ks.data_ptr(), vs.data_ptr(), slots.data_ptr(), T, Hkv, D, BS, NB, code)
-
-
 def reshape_and_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales,
                             slot_mapping, *, stream=None) -> None:
     """reshape_and_cache into an MXFP4 cache (pa_reshape_and_cache_mxfp4): key/value
     [T, Hkv, D] f16|bf16, planes as mxfp4_cache makes them, slot_mapping int32 [T]
     (negative = skip)."""
-    _mxfp4_rows(_native.lib().pa_reshape_and_cache_mxfp4, key, value, key_cache, value_cache,
-                k_scales, v_scales, slot_mapping, stream)
+    status = _native.tensors().write_rows(key, value, key_cache, value_cache, k_scales, v_scales,
+                                          slot_mapping, _handle(stream))
+    if status:
+        check(status)
 
 
 def gather_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, *,
@@ -379,8 +279,10 @@ def gather_cache_mxfp4(key, value, key_cache, value_cache, k_scales, v_scales, s
     """Rows of an MXFP4 cache by slot into key/value [T, Hkv, D] f16|bf16
     (pa_gather_cache_mxfp4); rows whose slot is negative or outside the pool stay
     as they were."""
-    _mxfp4_rows(_native.lib().pa_gather_cache_mxfp4, key, value, key_cache, value_cache,
-                k_scales, v_scales, slot_mapping, stream)
+    status = _native.tensors().read_rows(key, value, key_cache, value_cache, k_scales, v_scales,
+                                         slot_mapping, _handle(stream))
+    if status:
+        check(status)
 
 
 def decode_mxfp4(out, query, key_cache, value_cache, k_scales, v_scales, block_tables,
@@ -389,20 +291,16 @@ def decode_mxfp4(out, query, key_cache, value_cache, k_scales, v_scales, block_t
     """decode over an MXFP4 cache (pa_decode_mxfp4): out/query [S, H, D] f16|bf16, planes as
     mxfp4_cache makes them; workspace from decode_workspace(..., cache_dtype=PA_MXFP4).
     Returns ``out``."""
-    code, (S, H, D), dev = _check_pair(query, out, "query", "out")
-    NB, Hkv, BS = _check_mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D, dev)
-    _, width = _check_table("block_tables", block_tables, S, dev)
-    _check_ints("context_lens", context_lens, (S,), dev)
     if workspace is None:
-        workspace = _own_workspace(lambda: decode_workspace(
-            S, H, Hkv, D, BS, max_context_len, partition_tokens, stream=stream,
-            cache_dtype=PA_MXFP4), dev, stream)
-    ws, ws_bytes = _check_workspace(workspace, dev)
-    _launch(_native.lib().pa_decode_mxfp4, dev, stream, out.data_ptr(), query.data_ptr(),
-            key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
-            int(max_context_len), S, H, Hkv, D, BS, NB, float(scale), code,
-            int(partition_tokens), ws, ws_bytes)
+        S, H, D = query.shape
+        workspace = _own_workspace(query, stream, lambda: decode_workspace(
+            S, H, key_cache.shape[1], D, key_cache.shape[2], max_context_len, partition_tokens,
+            stream=stream, cache_dtype=PA_MXFP4))
+    status = _native.tensors().decode(out, query, key_cache, value_cache, k_scales, v_scales,
+                                      block_tables, context_lens, max_context_len, scale,
+                                      partition_tokens, workspace, _handle(stream))
+    if status:
+        check(status)
     return out
 
 
@@ -412,21 +310,16 @@ def chunked_prefill_mxfp4(out, query, cu_query_lens, max_query_len: int, key_cac
     """chunked_prefill over an MXFP4 cache (pa_chunked_prefill_mxfp4): out/query [T, H, D]
     f16|bf16, planes as mxfp4_cache makes them; workspace from
     chunked_prefill_workspace(..., PA_MXFP4). Returns ``out``."""
-    code, (T, H, D), dev = _check_pair(query, out, "query", "out")
-    NB, Hkv, BS = _check_mxfp4_planes(key_cache, value_cache, k_scales, v_scales, D, dev)
-    S, width = _check_table("block_tables", block_tables, None, dev)
-    _check_ints("context_lens", context_lens, (S,), dev)
-    _check_ints("cu_query_lens", cu_query_lens, (S + 1,), dev)
     if workspace is None:
-        workspace = _own_workspace(lambda: chunked_prefill_workspace(
-            S, T, H, Hkv, D, max_query_len, max_context_len, PA_MXFP4, stream=stream), dev,
-            stream)
-    ws, ws_bytes = _check_workspace(workspace, dev)
-    _launch(_native.lib().pa_chunked_prefill_mxfp4, dev, stream, out.data_ptr(),
-            query.data_ptr(), cu_query_lens.data_ptr(), T, int(max_query_len),
-            key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
-            int(max_context_len), S, H, Hkv, D, BS, NB, float(scale), code, ws, ws_bytes)
+        T, H, D = query.shape
+        workspace = _own_workspace(query, stream, lambda: chunked_prefill_workspace(
+            context_lens.shape[0], T, H, key_cache.shape[1], D, max_query_len, max_context_len,
+            PA_MXFP4, stream=stream))
+    status = _native.tensors().chunked_prefill(
+        out, query, cu_query_lens, max_query_len, key_cache, value_cache, k_scales, v_scales,
+        block_tables, context_lens, max_context_len, scale, workspace, _handle(stream))
+    if status:
+        check(status)
     return out
 
 
@@ -454,15 +347,10 @@ class CachePool:
         self.planes = planes
         self.block_size = int(block_size)
         self.num_blocks = int(first.shape[0])
-        self._dev = first.get_device()
         self._array = (_native.Plane * len(planes))(
-            *[_native.Plane(t.data_ptr(), t.stride(0) * t.element_size()) for t in planes])
-
-    def _word(self, error_word):
-        if error_word is None:
-            return None
-        _check_ints("error_word", error_word, (1,), self._dev)
-        return error_word.data_ptr()
+            *[_native.Plane(t.data_ptr(), t[0].numel() * t.element_size()) for t in planes])
+        self._args = (ctypes.addressof(self._array), len(planes), self.num_blocks,
+                      first.get_device())
 
     def fork(self, block_tables, context_lens, parents, fresh_blocks, new_block_tables,
              new_context_lens, *, error_word=None, stream=None) -> None:
@@ -470,32 +358,19 @@ class CachePool:
         parent's whole blocks; a last block that is not full is copied into block
         fresh_blocks[i] of every plane (a negative entry shares it). Writes
         new_block_tables int32 [n, max_blocks_per_seq] and new_context_lens int32 [n]."""
-        dev = self._dev
-        S, width = _check_table("block_tables", block_tables, None, dev)
-        n = parents.numel()
-        _check_ints("context_lens", context_lens, (S,), dev)
-        _check_ints("parents", parents, (n,), dev)
-        _check_ints("fresh_blocks", fresh_blocks, (n,), dev)
-        _check_ints("new_block_tables", new_block_tables, (n, width), dev)
-        _check_ints("new_context_lens", new_context_lens, (n,), dev)
-        _launch(_native.lib().pa_fork_sequences, dev, stream, self._array, len(self.planes),
-                self.num_blocks, self.block_size, block_tables.data_ptr(), S, width,
-                context_lens.data_ptr(), parents.data_ptr(), fresh_blocks.data_ptr(), n,
-                new_block_tables.data_ptr(), new_context_lens.data_ptr(),
-                self._word(error_word))
+        status = _native.tensors().fork(*self._args, self.block_size, block_tables, context_lens,
+                                        parents, fresh_blocks, new_block_tables,
+                                        new_context_lens, error_word, _handle(stream))
+        if status:
+            check(status)
 
     def compact(self, moves, block_tables=None, *, error_word=None, stream=None) -> None:
         """Move blocks moves[i, 0] -> moves[i, 1] in every plane and rename them in
         block_tables, in place (pa_compact_blocks; BlockAllocator.compact makes the list)."""
-        dev = self._dev
-        n = moves.shape[0] if moves.dim() else 0
-        _check_ints("moves", moves, (n, 2), dev)
-        table, entries = None, 0
-        if block_tables is not None:
-            _check_table("block_tables", block_tables, None, dev)
-            table, entries = block_tables.data_ptr(), block_tables.numel()
-        _launch(_native.lib().pa_compact_blocks, dev, stream, self._array, len(self.planes),
-                self.num_blocks, moves.data_ptr(), n, table, entries, self._word(error_word))
+        status = _native.tensors().compact(*self._args, moves, block_tables, error_word,
+                                           _handle(stream))
+        if status:
+            check(status)
 
 
 def sha256(data: bytes) -> bytes:

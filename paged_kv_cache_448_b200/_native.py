@@ -114,6 +114,21 @@ def _load() -> ctypes.CDLL:
         return _lib
 
 
+_tensors = None
+
+
+def tensors():
+    """The module _tensors (binding/tensors.cpp): calls that take torch tensors
+    directly (raises if it has not been built)."""
+    global _tensors
+    if _tensors is None:
+        import torch  # noqa: F401  (its libraries first)
+        lib()
+        from . import _tensors as module
+        _tensors = module
+    return _tensors
+
+
 def check(status: int) -> None:
     if status != PA_OK:
         msg = lib().pa_last_error()

@@ -5,7 +5,9 @@
 Every source under csrc/ is compiled to an object in <repo>/_build/ (in
 parallel), then linked into paged_kv_cache_448_b200/libpaged.so with the CUDA
 runtime linked statically. An object is rebuilt when its source or any header
-is newer than it.
+is newer than it. binding/tensors.cpp, the calls that take torch tensors
+directly, becomes paged_kv_cache_448_b200/_tensors.so against the installed
+torch's headers (g++).
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpaged.so")
+BINDING = os.path.join(PKG, "binding", "tensors.cpp")
+TENSORS = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden,-Wall",
@@ -80,7 +85,33 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     if verbose:
         for src, log in sorted(logs):
             sys.stderr.write(f"== {os.path.basename(src)}\n{log}")
+    build_binding(force)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """_tensors.so, when it is older than its source, the C header or torch."""
+    import torch
+    from torch.utils import cpp_extension
+    inputs = [BINDING, os.path.join(INCLUDE, "paged.h"), torch.__file__]
+    if not force and os.path.exists(TENSORS) and \
+            os.path.getmtime(TENSORS) >= max(os.path.getmtime(f) for f in inputs):
+        return TENSORS
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = TENSORS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda]
+    for inc in cpp_extension.include_paths():
+        cmd += ["-isystem", inc]
+    cmd += [BINDING, "-o", tmp, "-L", PKG, "-l:libpaged.so", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(BINDING)}:\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
 
 
 def main():

@@ -45,8 +45,9 @@
 // memory as an E4M3 hi part and an E5M2 residual, so O += P V takes two
 // 8-bit MMAs with V read MN-major; the V scale applies in the epilogue.
 // An MXFP4 cache (mxfp4.cuh) is widened to f16 on its way into shared memory:
-// in place of the TMA warps, seven converter warps load codes and scales into
-// registers, some items ahead (an item is 16 rows), and once the MMAs that read a stage completed they write
+// in place of the TMA warps, four converter warps per ring load codes and
+// scales into registers, a step ahead, and once the MMAs that read a stage
+// completed they write
 // code * 2^(b - r + 13) into it in the layout the TMA boxes have. From there on
 // it is the f16 kernel. r is a reference for the scales, undone in the logit
 // scale and the epilogue: with an f16 query 140 (the values themselves), with a
@@ -106,16 +107,19 @@ struct TcCfg {
   static constexpr bool MX = std::is_same<CF, Mxfp4>::value;
   static constexpr bool OBF = std::is_same<QF, BF16>::value;  // query and output
   static constexpr bool BF = OBF && !MX;                      // MMA operands
-  // warps besides the softmax warps: MMA issue, then the loaders
-  static constexpr int CW = MX ? 7 : 2;
-  static constexpr int THREADS = NG * kTcRows + 32 + 32 * CW;
+  // warps besides the softmax warps: MMA issue, then the loaders (MXFP4: a
+  // warpgroup whose first warp issues the MMAs, and a warpgroup per ring)
+  static constexpr int CW = 4;
+  static constexpr int THREADS = NG * kTcRows + (MX ? 384 : 96);
   // MXFP4: registers per thread at launch (what __launch_bounds__ leaves), of
-  // the softmax warps and of the other eight; the same total before and after
-  static constexpr int LAUNCH_REGS = NG == 2 ? 128 : 80;
-  static constexpr int SOFTMAX_REGS = NG == 2 ? 168 : 112;
-  static constexpr int OTHER_REGS = NG == 2 ? 88 : 64;
-  static_assert(!MX || (NG * kTcRows * SOFTMAX_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS &&
-                        THREADS == NG * kTcRows + 256),
+  // the softmax warps, the MMA warpgroup and the converter warps; no more in
+  // all after than before
+  static constexpr int LAUNCH_REGS = NG == 2 ? 96 : 64;
+  static constexpr int SOFTMAX_REGS = NG == 2 ? 144 : 112;
+  static constexpr int MMA_REGS = NG == 2 ? 72 : 32;
+  static constexpr int CONVERTER_REGS = 56;
+  static_assert(!MX || NG * kTcRows * SOFTMAX_REGS + 128 * MMA_REGS + 256 * CONVERTER_REGS <=
+                           THREADS * LAUNCH_REGS,
                 "register shares");
   static constexpr int NSEG = D * CF::kBytes / 128;  // 128-byte segments of a cache row
   static_assert(NSEG >= 1, "rows of at least 128 bytes");
@@ -177,6 +181,14 @@ __device__ __forceinline__ uint32_t pack_pair(bool bf, float lo, float hi) {
   return bf ? pack2<true>(lo, hi) : pack2<false>(lo, hi);
 }
 
+// True in one lane of a converged warp; the compiler then knows that one thread
+// runs what follows, and keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // Two 16-bit query values (low half first) as floats.
 template <class QF>
 __device__ __forceinline__ float2 unpack_q(uint32_t w) {
@@ -213,25 +225,40 @@ constexpr int kOrderSeqs = 256;  // launches of up to this many sequences are re
 // The sequence of rank `rank` when the sequences are ordered by context length,
 // longest first (ties by index): sequence i has rank #{j : len_j > len_i} +
 // #{j < i : len_j == len_i}, a permutation for any lengths. Launches of more
-// than kOrderSeqs sequences keep their order (rank = sequence). Every thread of
-// the CTA calls it (two barriers).
-__device__ __forceinline__ int sequence_of_rank(const int32_t* context_lens, int n, int rank,
-                                                int32_t* lens, int* pick) {
-  if (n > kOrderSeqs) return rank;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) lens[i] = context_lens[i];
+// than kOrderSeqs sequences keep their order (rank = sequence). Returns the
+// sequence's context length and query rows as well; up to kOrderSeqs sequences
+// they come from shared memory, so that the launch waits for one load, and
+// eight lanes count a sequence's rank. Every thread of the CTA calls it (two
+// barriers).
+struct Unit {
+  int s, q0, qlen, ctx;
+};
+__device__ __forceinline__ Unit unit_of_rank(const int32_t* context_lens, const int32_t* cu, int n,
+                                             int rank, int32_t* lens, int32_t* starts, int* pick) {
+  if (n > kOrderSeqs)
+    return {rank, cu[rank], cu[rank + 1] - cu[rank], context_lens[rank]};
+  for (int i = threadIdx.x; i <= n; i += blockDim.x) {
+    if (i < n) lens[i] = context_lens[i];
+    starts[i] = cu[i];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int32_t li = lens[i];
+  const int part = threadIdx.x % 8;
+  for (int i0 = 0; i0 < n; i0 += static_cast<int>(blockDim.x) / 8) {  // whole warps stay
+    const int i = i0 + static_cast<int>(threadIdx.x) / 8;
+    const int32_t li = i < n ? lens[i] : 0;
     int r = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
+    for (int j = part; j < n; j += 8) {
       const int32_t lj = lens[j];
       r += (lj > li) | ((lj == li) & (j < i));
     }
-    if (r == rank) *pick = i;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) r += __shfl_xor_sync(0xffffffffu, r, d);
+    if (part == 0 && i < n && r == rank) *pick = i;
   }
   __syncthreads();
-  return *pick;
+  const int s = *pick;
+  return {s, starts[s], starts[s + 1] - starts[s], lens[s]};
 }
 
 // Where the cache is: tensor maps of one-segment boxes, or the planes of an
@@ -299,7 +326,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   constexpr int NSEG = C::NSEG, QT = C::QT, KR = C::KR, VR = C::VR, NT = C::NT, TR = kTileRows;
   constexpr int SB = C::SB, H = C::H;
   constexpr int kMma = NG * kTcRows / 32;   // warp issuing the MMAs (owns the tensor memory)
-  constexpr int kLoader = kMma + 1;         // loader warps (TMA: K's, then V's)
+  constexpr int kLoader = kMma + (MX ? 4 : 1);  // loader warps: K's, then V's
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -315,18 +342,18 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       pv_bar[NG][2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int aborted;
-  __shared__ int32_t order_lens[kOrderSeqs];
+  __shared__ int32_t order_lens[kOrderSeqs], order_starts[kOrderSeqs + 1];
   __shared__ int order_pick;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t lim = a.wait_limit_ns;
   if (tid == 0) {
     for (int r = 0; r < KR; ++r) {
-      mbar_init(&kfull[r], MX ? NT / TR : 1);
+      mbar_init(&kfull[r], MX ? C::CW : 1);
       mbar_init(&kempty[r], 1);
     }
     for (int r = 0; r < VR; ++r) {
-      mbar_init(&vfull[r], MX ? NT / TR : 1);
+      mbar_init(&vfull[r], MX ? C::CW : 1);
       mbar_init(&vempty[r], 1);
     }
     for (int g = 0; g < NG; ++g)
@@ -356,12 +383,13 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const int rank = static_cast<int>(lin / per_seq), in_seq = static_cast<int>(lin % per_seq);
   const int kvh = in_seq / static_cast<int>(gridDim.x), xi = in_seq % static_cast<int>(gridDim.x);
   const int z = a.q_tiles - 1 - xi % a.q_tiles, part = xi / a.q_tiles;
-  const int s = sequence_of_rank(a.context_lens, a.num_seqs, rank, order_lens, &order_pick);
+  const Unit unit = unit_of_rank(a.context_lens, a.cu_query_lens, a.num_seqs, rank, order_lens,
+                                 order_starts, &order_pick);
+  const int s = unit.s;
   const bool first_unit = z == 0 && part == 0 && kvh == 0 && s == 0;
 
-  const int q0 = a.cu_query_lens[s];
-  const int qlen = a.cu_query_lens[s + 1] - q0;
-  int ctx = a.context_lens[s];
+  const int q0 = unit.q0, qlen = unit.qlen;
+  int ctx = unit.ctx;
   if (ctx > a.ctx_limit || ctx < 0) {
     if (tid == 0 && z == 0 && kvh == 0) report(a.err, kErrContextClipped);
     ctx = ctx < 0 ? 0 : a.ctx_limit;
@@ -405,6 +433,28 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const int tend = min(ntiles_all, tbase + a.partition_tiles);
   const int kbase = tbase / (NT / TR);
   const int nsteps = (tend - tbase + NT / TR - 1) / (NT / TR);
+
+  // 16-bit Q: the rows are shared out over all warps, some whole rows a load
+  // (D / 8 lanes each). With a row per thread every load touched 32 lines, and
+  // the prologue took a fifth of a unit's time (8 100 of 61 500 cycles, chunks
+  // of 512 tokens). The loads leave before the waits below.
+  constexpr int LPR = D / 8, RPL = 32 / LPR, WARPS = C::THREADS / 32;
+  constexpr int QLOADS = FP8 ? 1 : (C::ROWS / RPL + WARPS - 1) / WARPS;
+  __shared__ int q_exp[MX && C::OBF ? C::ROWS : 1];  // power of two of a row
+  const int q_rows = dup ? 64 : C::ROWS;
+  uint4 qv[QLOADS];
+  if constexpr (!FP8) {
+#pragma unroll
+    for (int j = 0; j < QLOADS; ++j) {
+      const int r = (warp + j * WARPS) * RPL + lane / LPR;
+      qv[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < q_rows && r / G < ntok)
+        qv[j] = reinterpret_cast<const uint4*>(
+            static_cast<const uint8_t*>(a.query) +
+            (static_cast<int64_t>(q0 + tok0 + r / G) * a.num_heads + kvh * G + r % G) * D *
+                2)[lane % LPR];
+    }
+  }
 
   // MXFP4, bf16 query: the largest scale bytes of this CTA's keys and values
   // (255, a NaN block, aside; bytes of rows that are not there do not count)
@@ -465,53 +515,39 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     }
   }
   if (warp == kMma) tc::alloc(&tmem_slot, C::TMEM_COLS);
-  float qscale = a.scale_log2;  // logit scale of this thread's row (base 2)
-  if (warp < kMma) {
+  if constexpr (!FP8) {
     // Q rows -> shared memory (per group, 128-byte swizzle, K-major), zeros past the chunk
+    const int c = lane % LPR;
+#pragma unroll
+    for (int j = 0; j < QLOADS; ++j) {
+      const int r = (warp + j * WARPS) * RPL + lane / LPR;
+      uint4 v = qv[j];
+      if constexpr (MX && C::OBF) {
+        float mq = chunk_max(v);
+#pragma unroll
+        for (int d = 1; d < LPR; d *= 2) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, d));
+        const int field = static_cast<int>(__float_as_uint(mq) >> 23);
+        const int e = mq > 0.f && field < 255 ? min(max(127 - field, -126), 126) : 0;
+        v = scaled_f16(v, __uint_as_float(static_cast<uint32_t>(e + 127) << 23));
+        if (c == 0 && r < q_rows) {
+          q_exp[r] = e;
+          if (dup) q_exp[r + 64] = e;
+        }
+      }
+      if (r < q_rows) {
+        uint8_t* dst = sq(r / kTcRows) + c / 8 * C::QPART;
+        *reinterpret_cast<uint4*>(dst + sw128(r % kTcRows, c % 8)) = v;
+        if (dup) *reinterpret_cast<uint4*>(dst + sw128(r + 64, c % 8)) = v;
+      }
+    }
+    fence_proxy_async_smem();
+  }
+  float qscale = a.scale_log2;  // logit scale of this thread's row (base 2)
+  if (FP8 && warp < kMma) {
     const int g = tid / kTcRows, rr = tid % kTcRows;
     const uint4* q4 = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.query) +
                                                      row_off * 2);
-    if constexpr (!FP8) {
-      // a warp loads its 32 rows some whole rows at a time (D / 8 lanes each):
-      // with a row per thread every load touched 32 lines, and the prologue
-      // took a fifth of a unit's time (measured: 8 100 of 61 500 cycles,
-      // 512-token chunks)
-      constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of one load
-      constexpr int LOADS = 32 / RPL, BATCH = 8;
-      const int c = lane % LPR;
-      int qe = 0;  // MXFP4, bf16 query: power of two of this thread's own row
-#pragma unroll
-      for (int j0 = 0; j0 < LOADS; j0 += BATCH) {
-        uint4 v[BATCH];
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          const int r = warp * 32 + (j0 + j) * RPL + lane / LPR, u = dup ? r & 63 : r;
-          v[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (u / G < ntok)
-            v[j] = reinterpret_cast<const uint4*>(
-                static_cast<const uint8_t*>(a.query) +
-                (static_cast<int64_t>(q0 + tok0 + u / G) * a.num_heads + kvh * G + u % G) * D *
-                    2)[c];
-        }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          if constexpr (MX && C::OBF) {
-            float mq = chunk_max(v[j]);
-#pragma unroll
-            for (int d = 1; d < LPR; d *= 2) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, d));
-            const int field = static_cast<int>(__float_as_uint(mq) >> 23);
-            const int e = mq > 0.f && field < 255 ? min(max(127 - field, -126), 126) : 0;
-            v[j] = scaled_f16(v[j], __uint_as_float(static_cast<uint32_t>(e + 127) << 23));
-            const int er = __shfl_sync(0xffffffffu, e, lane % RPL * LPR);
-            if (lane / RPL == j0 + j) qe = er;
-          }
-          const int rg = (warp % 4) * 32 + (j0 + j) * RPL + lane / LPR;
-          *reinterpret_cast<uint4*>(sq(g) + c / 8 * C::QPART + sw128(rg, c % 8)) = v[j];
-        }
-      }
-      // (the exponents together: each alone may leave fp32's range)
-      if constexpr (MX && C::OBF) qscale = ldexpf(qscale, ref_k - kMxTrueRef - qe);
-    } else {
+    if constexpr (FP8) {
       // row maximum, then q * 2^e = hi + lo (E4M3 each), 16 dims per 16-byte chunk
       float mq = 0.f;
       if (valid) {
@@ -557,116 +593,107 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  // whole warpgroups: the eight other warps here, the softmax warps in their branch
-  if constexpr (MX) {
-    if (warp >= kMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-  }
+  // (the exponents together: each alone may leave fp32's range)
+  if constexpr (MX && C::OBF)
+    if (warp < kMma) qscale = ldexpf(qscale, ref_k - kMxTrueRef - q_exp[tid]);
 
   if (MX && warp >= kLoader) {
     if constexpr (MX) {
-      // ================= converter warps =================
+      // ================= converter warps: four of K, four of V =================
       constexpr int NB = D / 32, RPL = 32 / NB;  // blocks of a row, rows of one load
-      constexpr int SUB = TR / RPL;              // loads of an item (16 rows)
-      constexpr int ITEMS = NT / TR;             // items of a stage
-      constexpr int AHEAD = SUB == 2 ? 2 : 4;    // items in flight per warp
-      static_assert((ITEMS & (ITEMS - 1)) == 0, "whole chunks");
-      const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-      const int bs_log = a.block_size == 32 ? 5 : 4;
-      const int kv_end = min(ctx, tend * TR);  // end of this CTA's tokens
-      // lane -> (row of the load, block): eight lanes that store together
-      // write four rows x two blocks of one segment, in eight different
-      // 16-byte columns of the swizzled tile
-      const int lb = NB == 4 ? (lane >> 4) * 2 + (lane & 1) : (lane & 1);
-      const int lr = NB == 4 ? (lane >> 1) & 7 : lane >> 1;
-      // Item n of the CTA is item n % ITEMS of chunk c = n / ITEMS, the chunks
-      // in the order K0, K1 V0, K2 V1, ... (the K past the last step is empty).
-      // All of this is the same in a warp's lanes.
-      auto is_v = [](uint32_t n) { return n >= 2 * ITEMS && ((n / ITEMS) & 1) == 0; };
-      auto step_of = [&](uint32_t n) {
-        return static_cast<int>((n / ITEMS + 1) / 2) - (is_v(n) ? 1 : 0);
-      };
-      const uint32_t total = (2 * nsteps + 1) * ITEMS;
-      auto token = [&](uint32_t n) {
-        return (kbase + step_of(n)) * NT + static_cast<int>(n % ITEMS) * TR;
-      };
-      // block id of item n (of the last block where it has no tokens): a plain
-      // load, whose value is first looked at when the item's rows are loaded
-      auto load_id = [&](uint32_t n) { return __ldg(table + (min(token(n), kv_end - 1) >> bs_log)); };
-      // loads of item n, whose block is id; returns how many of its rows there
-      // are (rows past them read block 0, and get the scale byte 0 when used)
-      const int32_t cstride = a.num_kv_heads * a.block_size * (D / 2);  // bytes of a block
-      const int32_t sstride = a.num_kv_heads * a.block_size * NB;
-      const int32_t coff = (kvh * a.block_size + lr) * (D / 2) + lb * 16;
-      const int32_t soff = (kvh * a.block_size + lr) * NB + lb;
-      const uint32_t pool = static_cast<uint32_t>(a.num_blocks);
-      auto load = [&](uint32_t n, int32_t id, MxRaw<SUB>& raw) {
-        const int t = token(n);
-        const bool real = n < total && t < kv_end, known = static_cast<uint32_t>(id) < pool;
-        if (real && !known && lane == 0) report(a.err, kErrBadBlockId);
-        const int64_t b = known ? id : 0;
-        const int row = static_cast<int>(n % ITEMS) * TR & (a.block_size - 1);
-        const bool v = is_v(n);
-        const uint8_t* c = (v ? cache.codes[1] : cache.codes[0]) + (b * cstride + (coff + row * (D / 2)));
-        const uint8_t* sc = (v ? cache.scales[1] : cache.scales[0]) + (b * sstride + (soff + row * NB));
+      constexpr int SUB = TR / RPL;              // loads of a 16-row tile
+      constexpr int PER = NT / TR / C::CW;       // tiles of a step per warp
+      static_assert(PER * C::CW * TR == NT, "whole tiles");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONVERTER_REGS));
+      const int w = __shfl_sync(0xffffffffu, warp, 0) - kLoader;
+      {
+        const bool v = w >= C::CW;
+        const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+        const int bs_log = a.block_size == 32 ? 5 : 4;
+        const int kv_end = min(ctx, tend * TR);  // end of this CTA's tokens
+        // lane -> (row of the load, block): eight lanes that store together
+        // write four rows x two blocks of one segment, in eight different
+        // 16-byte columns of the swizzled tile
+        const int lb = NB == 4 ? (lane >> 4) * 2 + (lane & 1) : (lane & 1);
+        const int lr = NB == 4 ? (lane >> 1) & 7 : lane >> 1;
+        const int32_t cstride = a.num_kv_heads * a.block_size * (D / 2);  // bytes of a block
+        const int32_t sstride = a.num_kv_heads * a.block_size * NB;
+        const uint8_t* codes = cache.codes[v] + (kvh * a.block_size + lr) * (D / 2) + lb * 16;
+        const uint8_t* scales = cache.scales[v] + (kvh * a.block_size + lr) * NB + lb;
+        const int ref = v ? ref_v : ref_k;
+        uint64_t* full = v ? vfull : kfull;
+        uint64_t* empty = v ? vempty : kempty;
+        // this lane's places in a stage: tile w, its first load
+        uint8_t* const stage0 = (v ? sv(0) : sk(0)) + (lb / 2) * C::KV_SEG;
+        // tile i of step k covers the 16 tokens from token(k, i)
+        auto token = [&](int k, int i) { return (kbase + k) * NT + (w % C::CW + i * C::CW) * TR; };
+        // block id of a tile (of the last block where it has no tokens): a plain
+        // load, whose value is first looked at when the tile's rows are loaded
+        auto load_id = [&](int k, int i) {
+          return __ldg(table + (min(token(k, i), kv_end - 1) >> bs_log));
+        };
+        MxRaw<SUB> raw[PER];
+        int rows[PER];  // rows of the tile that are there (the others get the scale byte 0)
+        int32_t id[PER] = {};
+        auto load = [&](int k, int i) {
+          const int t = token(k, i);
+          const bool real = t < kv_end;
+          const bool known = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.num_blocks);
+          if (real && !known && lane == 0) report(a.err, kErrBadBlockId);
+          const int32_t b = known ? id[i] : 0;
+          const int row = t & (a.block_size - 1);
+          const uint8_t* c = codes + static_cast<int64_t>(b) * cstride + row * (D / 2);
+          const uint8_t* sc = scales + static_cast<int64_t>(b) * sstride + row * NB;
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) mx_load(raw, u, c + u * RPL * (D / 2), sc + u * RPL * NB);
-        return real && known ? kv_end - t : 0;
-      };
-      bool ok = true;
-      auto convert = [&](uint32_t n, const MxRaw<SUB>& raw, int rows) {
-        const int k = step_of(n), j = static_cast<int>(n % ITEMS);
-        if (k >= nsteps) return;  // (the K past the last step)
-        const bool v = is_v(n);
-        const int R = v ? VR : KR;
-        if (k >= R)
-          ok = __all_sync(0xffffffffu, mbar_wait(v ? &vempty[k % VR] : &kempty[k % KR],
-                                                 ((k - R) / R) & 1, lim, &aborted));
-        if (!ok) return;
-        const int t_begin = (kbase + k) * (NT / TR), t_end = min(tend, t_begin + NT / TR);
-        if (!v && a.skip_tile >= t_begin - tbase && a.skip_tile < t_end - tbase &&
-            skip_unit_for_test(a.skip_tile, a.skip_tile, first_unit))
-          return;  // (the step is never complete)
-        uint8_t* seg = (v ? sv(k) : sk(k)) + (lb / 2) * C::KV_SEG;
+          for (int u = 0; u < SUB; ++u)
+            mx_load(raw[i], u, c + u * RPL * (D / 2), sc + u * RPL * NB);
+          rows[i] = real && known ? kv_end - t : 0;
+        };
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          const int r = u * RPL + lr;
-          uint4 o[4];
-          mx_widen(raw.codes[u], r < rows ? static_cast<int>(raw.scale[u]) : 0, v ? ref_v : ref_k,
-                   o);
+        for (int i = 0; i < PER; ++i) id[i] = load_id(0, i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(seg + sw128(j * TR + r, (lb & 1) * 4 + i)) = o[i];
+        for (int i = 0; i < PER; ++i) {
+          load(0, i);
+          id[i] = load_id(1, i);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v ? &vfull[k % VR] : &kfull[k % KR]);
-      };
-      // this warp's items are w, w + CW, ...; slot i of the rotating registers
-      // holds the loads of item n + i CW, and the block id of item n + (i + AHEAD) CW
-      MxRaw<SUB> raw[AHEAD];
-      int rows[AHEAD];
-      int32_t id[AHEAD];
-      uint32_t n = __shfl_sync(0xffffffffu, warp, 0) - kLoader;
+        bool ok = true;
+        for (int k = 0; k < nsteps; ++k) {
+          static_assert(KR == 2 && VR == 2, "two stages");
+          if (k >= 2)
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty[k & 1], ((k >> 1) & 1) ^ 1, lim, &aborted));
+          if (!ok) break;
+          uint8_t* stage = stage0 + (k & 1) * C::KV_BYTES;
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) id[i] = load_id(n + i * C::CW);
+          for (int i = 0; i < PER; ++i) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        rows[i] = load(n + i * C::CW, id[i], raw[i]);
-        id[i] = load_id(n + (i + AHEAD) * C::CW);
-      }
-      for (; ok && n < total; n += AHEAD * C::CW) {
+            for (int u = 0; u < SUB; ++u) {
+              const int r = u * RPL + lr;
+              uint4 o[4];
+              mx_widen(raw[i].codes[u], r < rows[i] ? static_cast<int>(raw[i].scale[u]) : 0, ref, o);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          const uint32_t m = n + i * C::CW;
-          if (!ok || m >= total) break;
-          convert(m, raw[i], rows[i]);
-          rows[i] = load(m + AHEAD * C::CW, id[i], raw[i]);
-          id[i] = load_id(m + 2 * AHEAD * C::CW);
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(
+                    stage + sw128((w % C::CW + i * C::CW) * TR + r, (lb & 1) * 4 + j)) = o[j];
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int t_begin = (kbase + k) * (NT / TR), t_end = min(tend, t_begin + NT / TR);
+          const bool skip = !v && a.skip_tile >= t_begin - tbase && a.skip_tile < t_end - tbase &&
+                            skip_unit_for_test(a.skip_tile, a.skip_tile, first_unit);
+          if (lane == 0 && !skip) mbar_arrive(&full[k & 1]);  // (else the step is never complete)
+          if (k + 1 < nsteps) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              load(k + 1, i);
+              id[i] = load_id(k + 2, i);
+            }
+          }
         }
-      }
-      if (!ok && lane == 0) {
-        aborted = 1;
-        report(a.err, kErrWaitTimeout);
+        if (!ok && lane == 0) {
+          aborted = 1;
+          report(a.err, kErrWaitTimeout);
+        }
       }
       __syncwarp();  // whole warps reach the CTA barrier below
     }
@@ -734,9 +761,10 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       for (int j = max(0, issued - R); j < issued; ++j) mbar_wait(&full[j % R], (j / R) & 1, lim);
     __syncwarp();  // whole warps reach the CTA barrier below
     }
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     // ================= MMA issue (one thread) =================
-    if (lane == 0) {
+    if constexpr (MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::MMA_REGS));
+    if (warp == kMma && elect_one()) {
       // descriptors computed once; a k-step or stage offset is added to the
       // start-address field (bits 0-13, in 16-byte units)
       uint64_t qd[NG];
@@ -847,9 +875,10 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
         //  * S(k): K of step k landed and the S buffer is free, i.e. O += P V
         //    of step k - 2 (which read the P written over that S) completed;
         //  * O += P V (k): S(k) issued, P of step k posted, V landed.
-        // Gives up after the wait limit without progress.
-        int ns = 0, np = 0;
-        uint64_t t_last = global_timer_ns();
+        // Gives up after the wait limit without progress; the clock, whose
+        // reading takes longer than a poll, is looked at every 64 idle polls.
+        int ns = 0, np = 0, idle = 0;
+        uint64_t t_idle = 0;
         while (np < nsteps) {
           bool progress = false;
           if (np < ns && mbar_test_wait(&p_bar[0][np & 1], (np >> 1) & 1) &&
@@ -870,10 +899,14 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
             progress = true;
           }
           if (progress) {
-            t_last = global_timer_ns();
-          } else if (aborted || global_timer_ns() - t_last > lim) {
-            ok = false;
-            break;
+            idle = 0;
+          } else if (++idle % 64 == 0) {
+            const uint64_t now = global_timer_ns();
+            if (idle == 64) t_idle = now;
+            if (*static_cast<volatile int*>(&aborted) || now - t_idle > lim) {
+              ok = false;
+              break;
+            }
           }
         }
       }
