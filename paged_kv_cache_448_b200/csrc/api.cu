@@ -498,9 +498,15 @@ namespace {
 // tiles of each CTA are cut into parts of at least 256 tokens (16 tiles, whole
 // steps of the kernel) handled by separate CTAs and merged by a combine kernel.
 // An MXFP4 cache always runs on tcgen05, whose converter warps widen a code
-// once for all of a CTA's rows.
+// once for all of a CTA's rows. There 256 rows share each widened step, but
+// two CTAs of 128 rows on an SM hide one another's start, so they are taken
+// up to contexts of 4 096 tokens and where 256 rows a CTA would not fill the
+// GPU (32 heads, 512-token chunks, two groups against one: 16 contexts of 512
+// to 4 096 tokens 215 / 208 us, 64 of 512 506 / 472, 2 of 6 500 to 8 500 with
+// 8 kv-heads 171 / 179; 4 of 3 500 to 4 096, 162 / 186, goes the other way).
 struct PrefillPlan {
   bool tc;                  // tcgen05 kernel (rows on M), else mma.sync
+  bool two;                 // MXFP4 on tcgen05: two row groups (256 rows) per CTA
   int32_t q_tiles, partition_tiles, max_parts;
 };
 
@@ -513,7 +519,11 @@ PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t gr
 
   // query tokens per CTA: tcgen05 128 rows per group, two groups once the
   // chunks fill 256 rows; mma.sync 64 rows
-  const int32_t qt_tc = (rows >= 256 ? 256 : 128) / group;
+  p.two = rows >= 256;
+  if (p.two && cache_dtype == PA_MXFP4)
+    p.two = max_context_len > 4096 &&
+            num_seqs * ((rows + 255) / 256) * num_kv_heads >= sm_count();
+  const int32_t qt_tc = (p.two ? 256 : 128) / group;
   const int64_t tc_ctas = static_cast<int64_t>(num_seqs) * num_kv_heads *
                           ((max_query_len + qt_tc - 1) / qt_tc);
   p.tc = cache_dtype == PA_MXFP4 ||
@@ -529,7 +539,7 @@ PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t gr
   // two of one group, per SM) up to a wave - measured on B200, 64 CTAs of
   // 4 x 128-token chunks 325 -> 247 us, while 128 CTAs of one 512-token
   // chunk lost (326 -> 354 us); mma.sync about four waves of three per SM
-  const int64_t wave = (rows >= 256 ? 1LL : 2LL) * sm_count();
+  const int64_t wave = (p.two ? 1LL : 2LL) * sm_count();
   const int64_t want = p.tc ? wave : 4LL * sm_count() * 3;
   if (ctas >= (p.tc ? (wave + 1) / 2 : want) || max_tiles < 32) return p;
   const int64_t by_work = (want + ctas - 1) / ctas;
@@ -537,7 +547,7 @@ PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t gr
   if (parts <= 1) return p;
   // whole steps of the kernel: 4 tiles (64 tokens), 8 for the tcgen05 kernel
   // with two row groups (128 tokens)
-  const int32_t step_tiles = p.tc && rows >= 256 ? 8 : 4;
+  const int32_t step_tiles = p.tc && p.two ? 8 : 4;
   int32_t pt = (max_tiles + parts - 1) / parts;
   pt = (pt + step_tiles - 1) / step_tiles * step_tiles;
   p.partition_tiles = pt;
@@ -906,7 +916,7 @@ PA_API pa_status pa_chunked_prefill_mxfp4(
   return cuda_status(
       launch_prefill_mxfp4(a, {key_cache, value_cache, k_scales, v_scales},
                            q_dtype == PA_F16 ? kF16 : kBF16, head_dim, group, max_query_len,
-                           reinterpret_cast<cudaStream_t>(stream)),
+                           plan.two, reinterpret_cast<cudaStream_t>(stream)),
       "chunked_prefill_mxfp4");
 }
 

@@ -212,6 +212,7 @@ struct MxState {
   int ref[NB];         // r_b: scale byte the V scales are taken relative to (-1: none yet)
   uint32_t nan_blocks; // blocks of V with a NaN scale in the context
   bool low;            // a reference so low that the window below it holds the byte 0
+  uint32_t off;        // added to a row's scale bytes: 0x80 .. 0x8f within the window
 
   __device__ __forceinline__ void init(const DecodeArgs& a, const uint8_t* query, int group,
                                        int lane) {
@@ -269,6 +270,7 @@ struct MxState {
     }
     nan_blocks = 0u;
     low = true;
+    off = 0u;
   }
 
   // The NB scale bytes of a row.
@@ -337,33 +339,6 @@ struct MxState {
           vw[u][i][1] = t >> 16;
         }
       }
-    if constexpr (PARTIAL) {  // the last step of a unit
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (16 * u + 8 * i + 2 * c + j >= valid) vw[u][i][j] = 0u;
-          }
-    }
-    // exponent of 2^(bV - r_b) as an f16 exponent field, two tokens a word:
-    // bytes of blocks 0, 2 and 1, 3 as 16-bit halves, paired over the tokens
-    uint32_t ex[2][2][NB];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t e0 = vw[u][i][0] & 0x00ff00ffu, e1 = vw[u][i][1] & 0x00ff00ffu;
-        const uint32_t o0 = (vw[u][i][0] >> 8) & 0x00ff00ffu,
-                       o1 = (vw[u][i][1] >> 8) & 0x00ff00ffu;
-        ex[u][i][0] = prmt(e0, e1, 0x5410);
-        ex[u][i][1] = prmt(o0, o1, 0x5410);
-        if constexpr (NB == 4) {
-          ex[u][i][2] = prmt(e0, e1, 0x7632);
-          ex[u][i][3] = prmt(o0, o1, 0x7632);
-        }
-      }
     float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -376,25 +351,24 @@ struct MxState {
           x[u][i][j] = t;
           mx[j] = fmaxf(mx[j], t);
         }
-    if constexpr (PARTIAL) {  // rows that are not of the context: a scale within the window
+    if constexpr (PARTIAL) {  // rows that are not of the context: scales within the window
+      uint32_t in = 0u;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) in |= static_cast<uint32_t>(max(ref[b], 1)) << (8 * b);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t = valid - (16 * u + 8 * i + 2 * c);  // rows of this word that are
-            const uint32_t keep = t <= 0 ? 0u : t == 1 ? 0x0000ffffu : 0xffffffffu;
-            ex[u][i][b] = (ex[u][i][b] & keep) |
-                          (static_cast<uint32_t>(max(ref[b], 1)) * 0x10001u & ~keep);
-          }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (16 * u + 8 * i + 2 * c + j >= valid) vw[u][i][j] = in;
     }
     const bool lift =
-        mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || outside(ex) || ff;
+        mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || outside(vw) || ff;
     bool wide = low;  // V scales below the window (the same in every lane)
     if (__any_sync(FULL, lift)) {
-      update(x, mx, kw, ff, vw, ex);
-      wide = low || __any_sync(FULL, outside(ex));
+      update(x, mx, kw, ff, vw);
+      wide = low || __any_sync(FULL, outside(vw));
     }
     // ---- probabilities, their sum, and P as B operand (tokens x heads)
     const float mu0 = m[0] == -CUDART_INF_F ? 0.f : m[0];
@@ -411,13 +385,22 @@ struct MxState {
         p[u][i] = movm_trans(*reinterpret_cast<const uint32_t*>(&h));
       }
     if (wide) {  // the bands below the window; those tokens weigh nothing after this
-      bands<SWZ>(vc, p, ex, lane);
+      bands<SWZ>(vc, p, vw, lane);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) ex[u][i][b] = window_only(ex[u][i][b], ref[b]);
+          for (int j = 0; j < 2; ++j) {
+            uint32_t w = 0u;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const int v = byte_of(vw[u][i][j], b);
+              const bool in = v >= max(ref[b] - 8, 1) && v <= ref[b] + 7;
+              w |= static_cast<uint32_t>(in ? v : (ref[b] - 15) & 31) << (8 * b);  // factor 0
+            }
+            vw[u][i][j] = w;
+          }
     }
     // ---- O += V^T (P 2^(bV - r))
 #pragma unroll
@@ -426,7 +409,7 @@ struct MxState {
       load_codes<D, SWZ, true>(vc, u, lane, r);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t f0 = f16_pow2(ex[u][0][b], ref[b]), f1 = f16_pow2(ex[u][1][b], ref[b]);
+        const uint32_t f0 = factor(vw[u][0], b), f1 = factor(vw[u][1], b);
         uint32_t h[2][4];
         v_pairs(r[0][b], h[0]);
         v_pairs(r[1][b], h[1]);
@@ -437,20 +420,31 @@ struct MxState {
     }
   }
 
-  // Nonzero if some V scale of the step (exponents of ex) is not within
-  // [r_b - 8, r_b + 7] of its block's reference.
-  __device__ __forceinline__ uint32_t outside(const uint32_t (&ex)[2][2][NB]) const {
+  // Nonzero if some V scale of the step is not within [r_b - 8, r_b + 7] of its
+  // block's reference: whole words of scales at once (w + off has an upper
+  // nibble of 8 in every byte exactly when every byte is within its window).
+  __device__ __forceinline__ uint32_t outside(const uint32_t (&vw)[2][2][2]) const {
     uint32_t bits = 0u;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      // halves 0x8000 + (v - r + 8): no carry between them, 0x800x within the window
-      const uint32_t add = static_cast<uint32_t>(0x8000 + 8 - ref[b]) * 0x10001u;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) bits |= (ex[u][i][b] + add) ^ 0x80008000u;
-    }
-    return bits & 0xfff0fff0u;
+        for (int j = 0; j < 2; ++j) bits |= (vw[u][i][j] + off) ^ 0x80808080u;
+    return bits & (NB == 4 ? 0xf0f0f0f0u : 0x0000f0f0u);
+  }
+
+  // The V scales of block b of two tokens (words w) as halves.
+  static __device__ __forceinline__ uint32_t halves(const uint32_t (&w)[2], int b) {
+    return prmt(w[0], w[1], static_cast<uint32_t>(b | (b + 4) << 8)) & 0x00ff00ffu;
+  }
+
+  // f16 of 2^(bV - r_b) for the two tokens, both within the window: the byte
+  // twice in each half, so that no sum carries into the other; the five bits of
+  // the exponent field are kept.
+  __device__ __forceinline__ uint32_t factor(const uint32_t (&w)[2], int b) const {
+    const uint32_t v = prmt(w[0], w[1], static_cast<uint32_t>(b * 0x11 | (b + 4) * 0x1100));
+    return (v * 0x400u + static_cast<uint32_t>((15 - ref[b]) & 31) * 0x04000400u) & 0x7c007c00u;
   }
 
   // The step's tokens whose V scale lies below the window of its block: bands
@@ -458,7 +452,7 @@ struct MxState {
   // its own added to O in fp32.
   template <int SWZ>
   __device__ __forceinline__ void bands(const uint8_t* vc, const uint32_t (&p)[2][2],
-                                        const uint32_t (&ex)[2][2][NB], int lane) {
+                                        const uint32_t (&vw)[2][2][2], int lane) {
     constexpr int RB = D / 2;
     constexpr unsigned FULL = 0xffffffffu;
 #pragma unroll
@@ -470,7 +464,7 @@ struct MxState {
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t in = halves_within(ex[u][i][b], 1, hi);
+            const uint32_t in = halves_within(halves(vw[u][i], b), 1, hi);
             t = max(t, max(static_cast<int>(in & 0xffffu), static_cast<int>(in >> 16)));
           }
         t = max(t, __shfl_xor_sync(FULL, t, 1));
@@ -486,7 +480,8 @@ struct MxState {
           uint32_t h[2][4];
           v_pairs(r[0], h[0]);
           v_pairs(r[1], h[1]);
-          const uint32_t e0 = u ? ex[1][0][b] : ex[0][0][b], e1 = u ? ex[1][1][b] : ex[0][1][b];
+          const uint32_t e0 = u ? halves(vw[1][0], b) : halves(vw[0][0], b);
+          const uint32_t e1 = u ? halves(vw[1][1], b) : halves(vw[0][1], b);
           const uint32_t p0 = u ? p[1][0] : p[0][0], p1 = u ? p[1][1] : p[0][1];
           const uint32_t b0 = hmul2u(p0, band_pow2(e0, t));
           const uint32_t b1 = hmul2u(p1, band_pow2(e1, t));
@@ -505,8 +500,7 @@ struct MxState {
 
   // The scale references move to the largest V scale of the step; a NaN scale
   // is remembered for its block.
-  __device__ __forceinline__ void update_scales(const uint32_t (&vw)[2][2][2],
-                                                uint32_t (&ex)[2][2][NB]) {
+  __device__ __forceinline__ void update_scales(uint32_t (&vw)[2][2][2]) {
     constexpr unsigned FULL = 0xffffffffu;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -521,7 +515,7 @@ struct MxState {
             const int v = byte_of(vw[u][i][j], b);
             if (v == kMxNan) {
               bad = true;
-              ex[u][i][b] &= j ? 0x0000ffffu : 0xffff0000u;  // as 0: no weight
+              vw[u][i][j] &= ~(255u << (8 * b));  // as 0: no weight
             } else {
               t = max(t, v);
             }
@@ -540,16 +534,19 @@ struct MxState {
       }
     }
     low = false;
+    off = NB == 4 ? 0x88888888u : 0x00008888u;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) low |= ref[b] <= 8;
+    for (int b = 0; b < NB; ++b) {
+      low |= ref[b] <= 8;
+      off -= static_cast<uint32_t>(ref[b]) << (8 * b);
+    }
   }
 
   // A maximum or a scale reference has to move, or a scale is NaN (a K scale:
   // the token's logit is NaN for every head).
   __device__ __forceinline__ void update(float (&x)[2][2][2], float (&mx)[2],
                                          const uint32_t (&kw)[2][2], uint32_t ff,
-                                         const uint32_t (&vw)[2][2][2],
-                                         uint32_t (&ex)[2][2][NB]) {
+                                         uint32_t (&vw)[2][2][2]) {
     constexpr unsigned FULL = 0xffffffffu;
     if (ff) {
 #pragma unroll
@@ -575,7 +572,7 @@ struct MxState {
         m[j] = mx[j];
       }
     }
-    update_scales(vw, ex);
+    update_scales(vw);
   }
 
   // (m, l) of each head and O in true units to shared memory.
@@ -944,7 +941,7 @@ struct MxPlanes {
 };
 
 template <class QF, int D, int NW, bool BLOCKS_ON_N>
-__global__ void __launch_bounds__(NW * 32, BLOCKS_ON_N ? 4 : 3)
+__global__ void __launch_bounds__(NW * 32, 4)
     paged_decode_mxfp4_kernel(const DecodeArgs a, const MxPlanes planes) {
   using C = MxCfg<D, NW>;
   constexpr int R = C::R, RB = C::RB, SB = C::SB;

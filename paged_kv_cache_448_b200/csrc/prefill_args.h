@@ -66,9 +66,10 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, const CUtensorMap& kmap,
                               int head_dim, int group, int32_t max_query_len,
                               cudaStream_t stream);
 
-// The same over an MXFP4 cache; planes: K codes, V codes, K scales, V scales.
+// The same over an MXFP4 cache; planes: K codes, V codes, K scales, V scales;
+// two: 256 rows per CTA, else 128.
 cudaError_t launch_prefill_mxfp4(const PrefillArgs& a, const uint8_t* const (&planes)[4],
                                  int q_dtype, int head_dim, int group, int32_t max_query_len,
-                                 cudaStream_t stream);
+                                 bool two, cudaStream_t stream);
 
 }  // namespace paged

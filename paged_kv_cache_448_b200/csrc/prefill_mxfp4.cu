@@ -6,10 +6,8 @@ namespace paged {
 
 cudaError_t launch_prefill_mxfp4(const PrefillArgs& a, const uint8_t* const (&planes)[4],
                                  int q_dtype, int head_dim, int group, int32_t max_query_len,
-                                 cudaStream_t stream) {
+                                 bool two, cudaStream_t stream) {
   const TcCache<Mxfp4> cache{{planes[0], planes[1]}, {planes[2], planes[3]}};
-  // two row groups (256 rows) when the chunks fill them
-  const bool two = static_cast<int64_t>(max_query_len) * group >= 2 * kTcRows;
 #define PAGED_TC(QF, d, g)                                                              \
   if (head_dim == d && group == g)                                                      \
     return two ? launch_tc<QF, Mxfp4, d, g, 2>(a, cache, max_query_len, stream)         \

@@ -225,40 +225,25 @@ constexpr int kOrderSeqs = 256;  // launches of up to this many sequences are re
 // The sequence of rank `rank` when the sequences are ordered by context length,
 // longest first (ties by index): sequence i has rank #{j : len_j > len_i} +
 // #{j < i : len_j == len_i}, a permutation for any lengths. Launches of more
-// than kOrderSeqs sequences keep their order (rank = sequence). Returns the
-// sequence's context length and query rows as well; up to kOrderSeqs sequences
-// they come from shared memory, so that the launch waits for one load, and
-// eight lanes count a sequence's rank. Every thread of the CTA calls it (two
-// barriers).
-struct Unit {
-  int s, q0, qlen, ctx;
-};
-__device__ __forceinline__ Unit unit_of_rank(const int32_t* context_lens, const int32_t* cu, int n,
-                                             int rank, int32_t* lens, int32_t* starts, int* pick) {
-  if (n > kOrderSeqs)
-    return {rank, cu[rank], cu[rank + 1] - cu[rank], context_lens[rank]};
-  for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-    if (i < n) lens[i] = context_lens[i];
-    starts[i] = cu[i];
-  }
+// than kOrderSeqs sequences keep their order (rank = sequence). Every thread of
+// the CTA calls it (two barriers).
+__device__ __forceinline__ int sequence_of_rank(const int32_t* context_lens, int n, int rank,
+                                                int32_t* lens, int* pick) {
+  if (n > kOrderSeqs) return rank;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) lens[i] = context_lens[i];
   __syncthreads();
-  const int part = threadIdx.x % 8;
-  for (int i0 = 0; i0 < n; i0 += static_cast<int>(blockDim.x) / 8) {  // whole warps stay
-    const int i = i0 + static_cast<int>(threadIdx.x) / 8;
-    const int32_t li = i < n ? lens[i] : 0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int32_t li = lens[i];
     int r = 0;
 #pragma unroll 4
-    for (int j = part; j < n; j += 8) {
+    for (int j = 0; j < n; ++j) {
       const int32_t lj = lens[j];
       r += (lj > li) | ((lj == li) & (j < i));
     }
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) r += __shfl_xor_sync(0xffffffffu, r, d);
-    if (part == 0 && i < n && r == rank) *pick = i;
+    if (r == rank) *pick = i;
   }
   __syncthreads();
-  const int s = *pick;
-  return {s, starts[s], starts[s + 1] - starts[s], lens[s]};
+  return *pick;
 }
 
 // Where the cache is: tensor maps of one-segment boxes, or the planes of an
@@ -342,7 +327,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       pv_bar[NG][2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int aborted;
-  __shared__ int32_t order_lens[kOrderSeqs], order_starts[kOrderSeqs + 1];
+  __shared__ int32_t order_lens[kOrderSeqs];
   __shared__ int order_pick;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -383,13 +368,12 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   const int rank = static_cast<int>(lin / per_seq), in_seq = static_cast<int>(lin % per_seq);
   const int kvh = in_seq / static_cast<int>(gridDim.x), xi = in_seq % static_cast<int>(gridDim.x);
   const int z = a.q_tiles - 1 - xi % a.q_tiles, part = xi / a.q_tiles;
-  const Unit unit = unit_of_rank(a.context_lens, a.cu_query_lens, a.num_seqs, rank, order_lens,
-                                 order_starts, &order_pick);
-  const int s = unit.s;
+  const int s = sequence_of_rank(a.context_lens, a.num_seqs, rank, order_lens, &order_pick);
   const bool first_unit = z == 0 && part == 0 && kvh == 0 && s == 0;
 
-  const int q0 = unit.q0, qlen = unit.qlen;
-  int ctx = unit.ctx;
+  const int q0 = a.cu_query_lens[s];
+  const int qlen = a.cu_query_lens[s + 1] - q0;
+  int ctx = a.context_lens[s];
   if (ctx > a.ctx_limit || ctx < 0) {
     if (tid == 0 && z == 0 && kvh == 0) report(a.err, kErrContextClipped);
     ctx = ctx < 0 ? 0 : a.ctx_limit;
