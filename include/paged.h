@@ -375,7 +375,7 @@ PA_API pa_status pa_copy_blocks(const void* src_key_cache, const void* src_value
  * a block with an infinity or a NaN gets b = 255. key, value: [num_tokens,
  * num_kv_heads, head_dim] of kv_dtype (F16 or BF16). slot_mapping as in
  * pa_reshape_and_cache: a token whose slot is negative or outside the pool is
- * not written.
+ * not written; the others' slots are distinct.
  */
 PA_API pa_status pa_reshape_and_cache_mxfp4(const void* key, const void* value, uint8_t* key_cache,
                                             uint8_t* value_cache, uint8_t* k_scales,

@@ -242,15 +242,13 @@ def _handle(stream):
 
 
 def _own_workspace(like, stream, make):
-    """A workspace of one call's own, kept from reuse until `stream` has passed it."""
+    """A workspace of one call's own on `like`'s device, allocated for `stream` (memory that
+    the allocator hands out again only behind the call on that stream)."""
     import torch
     if not like.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    with torch.cuda.device(like.device):
-        ws = make()
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    with torch.cuda.device(like.device), torch.cuda.stream(stream):
+        return make()
 
 
 def mxfp4_cache(num_blocks, num_kv_heads, block_size, head_dim, device="cuda"):

@@ -535,6 +535,7 @@ PrefillPlan make_prefill_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t gr
   p.partition_tiles = max_tiles;
   p.max_parts = 1;
   const int64_t ctas = static_cast<int64_t>(p.q_tiles) * num_kv_heads * num_seqs;
+  if (ctas == 0) return p;
   // CTAs wanted: tcgen05 splits below half a wave (one CTA of two groups, or
   // two of one group, per SM) up to a wave - measured on B200, 64 CTAs of
   // 4 x 128-token chunks 325 -> 247 us, while 128 CTAs of one 512-token

@@ -69,6 +69,7 @@
 
 #include <math_constants.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "consumer_mma.cuh"
@@ -502,10 +503,16 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   if constexpr (!FP8) {
     // Q rows -> shared memory (per group, 128-byte swizzle, K-major), zeros past the chunk
     const int c = lane % LPR;
+    // maxima are taken of raw logits, and masked ones are -inf: a negative
+    // scale negates Q instead, a scale of 0 makes it 0
+    const uint32_t negate = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const uint32_t keep = a.scale_log2 == 0.f ? 0u : 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < QLOADS; ++j) {
       const int r = (warp + j * WARPS) * RPL + lane / LPR;
       uint4 v = qv[j];
+      v = make_uint4((v.x & keep) ^ negate, (v.y & keep) ^ negate, (v.z & keep) ^ negate,
+                     (v.w & keep) ^ negate);
       if constexpr (MX && C::OBF) {
         float mq = chunk_max(v);
 #pragma unroll
@@ -526,13 +533,15 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     }
     fence_proxy_async_smem();
   }
-  float qscale = a.scale_log2;  // logit scale of this thread's row (base 2)
+  // logit scale of this thread's row (base 2), positive (see Q's staging)
+  float qscale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   if (FP8 && warp < kMma) {
     const int g = tid / kTcRows, rr = tid % kTcRows;
     const uint4* q4 = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.query) +
                                                      row_off * 2);
     if constexpr (FP8) {
       // row maximum, then q * 2^e = hi + lo (E4M3 each), 16 dims per 16-byte chunk
+      const float sign = a.scale_log2 < 0.f ? -1.f : a.scale_log2 == 0.f ? 0.f : 1.f;
       float mq = 0.f;
       if (valid) {
 #pragma unroll
@@ -562,8 +571,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 f0 = unpack_q<QF>(w[2 * j]), f1 = unpack_q<QF>(w[2 * j + 1]);
-            tc::split_fp8x4<false>(ldexpf(f0.x, e), ldexpf(f0.y, e), ldexpf(f1.x, e),
-                               ldexpf(f1.y, e), hw[j], lw[j]);
+            tc::split_fp8x4<false>(ldexpf(sign * f0.x, e), ldexpf(sign * f0.y, e),
+                                   ldexpf(sign * f1.x, e), ldexpf(sign * f1.y, e), hw[j], lw[j]);
           }
         }
         *reinterpret_cast<uint4*>(sq(g) + sw128(rr, c)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
@@ -1260,10 +1269,14 @@ cudaError_t launch_tc(const PrefillArgs& a, const TcCache<CF>& cache, int32_t ma
   if constexpr (C::MX) {
     // the shares of the register file hold for the launch's total alone: with
     // less the softmax warps would wait for registers that never come
-    static const int regs = [&] {
+    static std::atomic<int> known{0};
+    int regs = known.load(std::memory_order_relaxed);
+    if (regs == 0) {
       cudaFuncAttributes at{};
-      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-    }();
+      e = cudaFuncGetAttributes(&at, kern);
+      if (e != cudaSuccess) return e;
+      known.store(regs = at.numRegs, std::memory_order_relaxed);
+    }
     if (regs < C::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
   }
   PrefillArgs b = a;

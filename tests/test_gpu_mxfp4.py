@@ -458,3 +458,83 @@ def test_chunk_wait_that_runs_out(qlens, ctxs):
     mx.check(out[qlens[0]:], ref[qlens[0]:], bound[qlens[0]:], "the other sequence")
     out, _ = run_chunk(q, cache, qlens, 0.1)
     mx.check(out, ref, bound, "the next call")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [-0.4, 0.0])
+def test_scales_of_any_sign(dtype, scale):
+    """A negative softmax scale (maxima are then the smallest products), and none at all."""
+    rng = np.random.default_rng(31)
+    ctxs = [300, 33, 120]
+    cache = mx.Cache(ctxs, 2, 128, 16, rng)
+    for qlens in ([1, 1, 1], [5, 3, 2], [150, 33, 100]):
+        q, qx = mx.query(rng, sum(qlens), 4, 128, dtype, amp=2.0)
+        ref, bound = mx.attention(qx, cache, qlens, scale, dtype)
+        # a logit is a sum of |q||k| scale < 2^9 in all, off by 2^-22 of that (see above)
+        bound = bound + 2.0 ** -11 * 6
+        mx.check(run_chunk(q, cache, qlens, scale)[0], ref, bound, "chunks")
+        if sum(qlens) == 3:
+            mx.check(run_decode(q, cache, scale)[0], ref, bound, "decode")
+
+
+def test_query_with_nan_stays_in_its_row():
+    rng = np.random.default_rng(32)
+    cache = mx.Cache([80, 40], 2, 128, 16, rng)
+    q, _ = mx.query(rng, 20, 4, 128, "bf16")
+    clean = run_chunk(q, cache, [15, 5], 0.1)[0].clone()
+    one = run_decode(q[:2].contiguous(), cache, 0.1)[0].clone()
+    q[1, 2, 5] = float("nan")
+    q[7, 0, 127] = float("inf")
+    out = run_chunk(q, cache, [15, 5], 0.1)[0]
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[1, 2] = bad[7, 0] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
+    out = run_decode(q[:2].contiguous(), cache, 0.1)[0]
+    bad = bad[:2]
+    bad[1, 2] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], one[~bad])
+
+
+def test_output_over_the_query():
+    rng = np.random.default_rng(33)
+    cache = mx.Cache([700, 40], 2, 64, 16, rng)
+    q, qx = mx.query(rng, 2, 8, 64, "f16")
+    planes = [mx.to_dev(p) for p in cache.planes]
+    want = run_decode(q, cache, 0.1, 256)[0]
+    x = q.clone()
+    pk.decode_mxfp4(x, x, *planes, i32(cache.table), i32(cache.ctxs), 700, 0.1,
+                    partition_tokens=256)
+    assert torch.equal(x, want)
+    want = run_chunk(q, cache, [1, 1], 0.1)[0]
+    x = q.clone()
+    pk.chunked_prefill_mxfp4(x, x, i32([0, 1, 2]), 1, *planes, i32(cache.table), i32(cache.ctxs),
+                             700, 0.1)
+    assert torch.equal(x, want)
+
+
+def test_repeated_calls_give_the_same_bits():
+    rng = np.random.default_rng(34)
+    ctxs = [int(c) for c in rng.integers(1, 3000, 24)]
+    cache = mx.Cache(ctxs, 2, 128, 16, rng)
+    q, _ = mx.query(rng, 24, 16, 128, "bf16")
+    a = [run_decode(q, cache, 0.1)[0].clone() for _ in range(3)]
+    b = [run_chunk(q, cache, [1] * 24, 0.1)[0].clone() for _ in range(3)]
+    assert all(torch.equal(x, a[0]) for x in a) and all(torch.equal(x, b[0]) for x in b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunks_of_long_contexts(D):
+    """Contexts beyond 4096 tokens with enough rows for two groups a CTA, bf16 and f16."""
+    rng = np.random.default_rng(35)
+    ctxs, qlens = [4150, 300], [260, 130]
+    cache = mx.Cache(ctxs, 40, D, 32, rng)
+    for dtype in ("f16", "bf16"):
+        q, qx = mx.query(rng, sum(qlens), 40, D, dtype)
+        out, _ = run_chunk(q, cache, qlens, 1 / math.sqrt(D))
+        heads = [0, 17, 39]
+        sub = mx.Cache.__new__(mx.Cache)
+        sub.__dict__.update(cache.__dict__)
+        for name in ("kc", "vc", "ks", "vs"):
+            setattr(sub, name, getattr(cache, name)[:, heads])
+        ref, bound = mx.attention(qx[:, heads], sub, qlens, 1 / math.sqrt(D), dtype)
+        mx.check(out[:, heads], ref, bound, f"long contexts, {dtype}")

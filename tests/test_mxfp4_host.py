@@ -267,3 +267,10 @@ def test_binding_refusals_without_a_gpu():
     for bad in ([], [kc, kc[:2]], [kc.transpose(1, 2)], [kc]):
         with pytest.raises(ValueError):
             pk.CachePool(bad, 16)
+
+
+def test_workspace_sizes_of_empty_calls():
+    for dt in (pk.PA_F16, pk.PA_FP8_E4M3, pk.PA_MXFP4):
+        assert pk.chunked_prefill_workspace_size(0, 0, 8, 2, 128, 0, 4096, dt) == 256
+        assert pk.chunked_prefill_workspace_size(4, 0, 8, 2, 128, 0, 4096, dt) == 256
+        assert pk.decode_workspace_size(0, 8, 2, 128, 16, 4096, cache_dtype=dt) >= 256
