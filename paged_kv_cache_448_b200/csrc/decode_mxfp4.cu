@@ -40,6 +40,12 @@
 // A bf16 query row is scaled by a power of two that puts its largest element
 // in [1, 2) and held in f16: exact for elements down to 2^-17 of the largest,
 // an error of at most 2^-25 of it below.
+//
+// Bound by instruction issue, not by memory: a step of 32 tokens takes 650
+// (850 with MxState) instructions a warp, of which the conversions are 128. On
+// a B200, 32 sequences of 2 030 tokens with 32 heads, f16: 68 us, 4.15 TB/s of
+// codes and scales (an E4M3 cache 89 us, 16 bit 155); 24 sequences of 1 024 to
+// 32 768 tokens, 64 query heads on 8, bf16: 93 us (140 and 152).
 #include <math_constants.h>
 
 #include <type_traits>

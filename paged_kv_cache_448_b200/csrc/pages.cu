@@ -15,7 +15,9 @@
 // of 8 heads), so a launch per layer would cost more than the copies. The
 // work is cut into items of at most 4 KB of one block of one plane, one warp
 // each, all its loads in flight before the first store; the planes' pointers
-// travel in the launch's arguments.
+// travel in the launch's arguments. On a B200: 700 blocks of 4 layers of 32
+// heads in 16 bits (1.47 GB) 244 us, 6.0 TB/s; 128 partial blocks of 32 layers
+// in 4 bits (94 MB) 18 us; a few blocks 4 us, the launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
