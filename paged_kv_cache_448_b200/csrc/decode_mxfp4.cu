@@ -45,7 +45,7 @@
 // (850 with MxState) instructions a warp, of which the conversions are 128. On
 // a B200, 32 sequences of 2 030 tokens with 32 heads, f16: 68 us, 4.15 TB/s of
 // codes and scales (an E4M3 cache 89 us, 16 bit 155); 24 sequences of 1 024 to
-// 32 768 tokens, 64 query heads on 8, bf16: 93 us (140 and 152).
+// 32 768 tokens, 64 query heads on 8, bf16: 90 us (140 and 152).
 #include <math_constants.h>
 
 #include <type_traits>
@@ -112,6 +112,13 @@ __device__ __forceinline__ float fast_ex2(float x) {
 // 2^n, 0 below the normal numbers.
 __device__ __forceinline__ float pow2i(int n) {
   return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
+}
+
+// e such that mq 2^e lies in [1, 2) (2^e and 2^-e normal numbers; 0 for a row
+// of zeros or one that is not finite).
+__device__ __forceinline__ int row_exponent(float mq) {
+  const int field = static_cast<int>(__float_as_uint(mq) >> 23);
+  return mq > 0.f && field < 255 ? min(max(127 - field, -126), 126) : 0;
 }
 
 // Each 16-bit half v of x where lo <= v <= hi, the other halves as 0.
@@ -242,8 +249,9 @@ struct MxState {
     if constexpr (std::is_same<QF, BF16>::value) {
       mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
       mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
-      if (mq > 0.f && isfinite(mq)) e = -max(ilogbf(mq), -126);
+      e = row_exponent(mq);
     }
+    const float up = pow2i(e);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
@@ -251,7 +259,7 @@ struct MxState {
       for (int j = 0; j < 4; ++j) {
         if constexpr (std::is_same<QF, BF16>::value) {
           const float2 f = cvt2(BF16{}, x[j]);
-          const __half2 h = __floats2half2_rn(ldexpf(f.x, e), ldexpf(f.y, e));
+          const __half2 h = __floats2half2_rn(f.x * up, f.y * up);
           q[b][j] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
           q[b][j] = x[j];
@@ -261,8 +269,7 @@ struct MxState {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int eh = __shfl_sync(0xffffffffu, e, (2 * c + i) * 4);
-      // -e is undone in two factors, each a normal number
-      qs[i] = a.scale_log2 * ldexpf(1.f, -(eh / 2)) * ldexpf(1.f, eh / 2 - eh);
+      qs[i] = a.scale_log2 * pow2i(-eh);
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
     }
@@ -652,11 +659,12 @@ struct MxStateN {
       }
 #pragma unroll
       for (int d = 1; d < 4 * NB; d *= 2) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, d));
-      if (mq > 0.f && isfinite(mq)) e = -max(ilogbf(mq), -126);
+      e = row_exponent(mq);
+      const float up = pow2i(e);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = cvt2(BF16{}, x[j]);
-        const __half2 h = __floats2half2_rn(ldexpf(f.x, e), ldexpf(f.y, e));
+        const __half2 h = __floats2half2_rn(f.x * up, f.y * up);
         x[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
@@ -671,7 +679,7 @@ struct MxStateN {
         for (int j = 0; j < 4; ++j) o[b][i][j] = 0.f;
     }
     const int eh = __shfl_sync(0xffffffffu, e, head_of(2 * c) * NB * 4);
-    qs = a.scale_log2 * ldexpf(1.f, -(eh / 2)) * ldexpf(1.f, eh / 2 - eh);
+    qs = a.scale_log2 * pow2i(-eh);
     m = -CUDART_INF_F;
     l = 0.f;
     own = -1;
@@ -1030,7 +1038,8 @@ __global__ void __launch_bounds__(NW * 32, 4)
 
   typename std::conditional<BLOCKS_ON_N, MxStateN<QF, D>, MxState<QF, D>>::type st;
   const int64_t row0 = static_cast<int64_t>(s) * a.num_heads + kvh * group;
-  st.init(a, static_cast<const uint8_t*>(a.query) + row0 * D * 2, group, lane);
+  if (my_count > 0)  // (a warp without steps has nothing to set up or to hand over)
+    st.init(a, static_cast<const uint8_t*>(a.query) + row0 * D * 2, group, lane);
   for (int k = 0; k < my_count; ++k) {
     copy_wait<R - 1>();
     __syncwarp();  // every lane's copies of the step
@@ -1053,7 +1062,12 @@ __global__ void __launch_bounds__(NW * 32, 4)
   const bool single = parts == 1;
   float* mbuf = reinterpret_cast<float*>(smem);  // [NW][8][2]: m, l
   float* obuf = mbuf + NW * 16;                  // [NW][8][D]
-  st.finish(mbuf + warp * 16, obuf + warp * 8 * D, group, lane);
+  if (my_count > 0) {
+    st.finish(mbuf + warp * 16, obuf + warp * 8 * D, group, lane);
+  } else if (lane < group) {
+    mbuf[warp * 16 + 2 * lane] = -CUDART_INF_F;
+    mbuf[warp * 16 + 2 * lane + 1] = 0.f;
+  }
   __syncthreads();
   for (int idx = threadIdx.x; idx < group * D; idx += NW * 32) {
     const int h = idx / D, d = idx % D;
@@ -1068,7 +1082,8 @@ __global__ void __launch_bounds__(NW * 32, 4)
       // NaN logits has m = -inf and l = NaN, which must survive
       const float f = mw == -CUDART_INF_F ? (lw == 0.f ? 0.f : 1.f) : exp2f(mw - M);
       L += lw * f;
-      o += obuf[(w * 8 + h) * D + d] * f;
+      const float v = obuf[(w * 8 + h) * D + d];  // (not written by a warp without steps)
+      o = f != 0.f ? fmaf(v, f, o) : o;
     }
     o = L == 0.f ? 0.f : o / L;
     if (single) {
