@@ -118,9 +118,9 @@ constexpr int32_t kMaxParts = 65535;  // partitions per sequence (grid z extent)
 // units. The other decode kernels (three CTAs per SM) want about four waves.
 // The MXFP4 kernel (four CTAs per SM) is cut only where the sequences x
 // kv-heads are below one wave, then like the others: 1 024 units of 2 048
-// tokens 69 us in one pass, 74 / 82 us with partitions of 1 024 / 512; 192
-// units of 1 024 to 32 768 tokens 99 us with 2 048, 107 / 112 us with 4 096 /
-// 1 024.
+// tokens 67 us in one pass, 73 / 80 us with partitions of 1 024 / 512; 192
+// units of 1 024 to 32 768 tokens 92 us with 2 048, 98 / 99 us with 1 280 /
+// 2 816.
 Plan make_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
                int32_t max_context_len, int32_t requested, bool fp8_tc, bool mxfp4 = false) {
   const int32_t blocks_max = std::max<int32_t>(1, (max_context_len + block_size - 1) / block_size);

@@ -954,6 +954,8 @@ struct MxPlanes {
   const uint8_t* p[4];
 };
 
+// Four CTAs (16 warps) per SM: 128 registers a thread; with five the state
+// spills (32 x 32 heads x 2 030 tokens 82 us against 67), with three 75.
 template <class QF, int D, int NW, bool BLOCKS_ON_N>
 __global__ void __launch_bounds__(NW * 32, 4)
     paged_decode_mxfp4_kernel(const DecodeArgs a, const MxPlanes planes) {
@@ -1117,6 +1119,8 @@ cudaError_t decode_mxfp4(const DecodeArgs& a, const uint8_t* const (&planes)[4],
                          int head_dim, cudaStream_t stream) {
   const MxPlanes pl{{planes[0], planes[1], planes[2], planes[3]}};
   const int group = a.num_heads / a.num_kv_heads;
+  // blocks on the columns of N wherever heads x blocks fit there (32 kv-heads of
+  // one head each, 32 x 2 030 tokens: 101 us against 117 at that stage)
   const bool n = group * (head_dim / 32) <= 8;
 #define PAGED_MX(QT, QF, d)                                                     \
   if (q_dtype == QT && head_dim == d)                                          \

@@ -9,8 +9,8 @@
 // kv-head's group); NG = 2 once the chunks fill 256 rows) and 4 NG + 3 warps.
 // A step is 128 tokens with two groups (S = Q K^T with N = 128), 64 with one:
 //  * softmax warps, 4 per group: one row per thread and per tensor-memory
-//    lane. They write Q once into shared memory (128-byte swizzled, K-major),
-//    then per step load their row of S from tensor memory (the maximum first,
+//    lane. (Q is written once into shared memory, 128-byte swizzled, K-major:
+//    by all warps, or for an E4M3 cache by these.) Per step they load their row of S from tensor memory (the maximum first,
 //    then the probabilities), mask tokens after the row's position, and run
 //    the base-2 online softmax with a lazily updated maximum (it moves only
 //    when a row's maximum grows by more than 8, so probabilities stay below
