@@ -540,14 +540,15 @@ __global__ void __launch_bounds__(128) paged_prefill_combine(const PrefillArgs a
   for (int p = 0; p < parts; ++p) {
     const float2 v = ml[p];
     // a part that saw no token of this row (or gave up) has no weight, and
-    // its o may never have been written: it is not read
-    if (v.x == -CUDART_INF_F || !(v.y > 0.f)) continue;
+    // its o may never have been written: it is not read. A NaN sum (a NaN key
+    // or query, with any maximum) is no such part: the row becomes NaN.
+    if (v.y == 0.f) continue;
     const float w = v.y * exp2f(v.x - M);
     L += w;
 #pragma unroll
     for (int j = 0; j < PER; ++j) acc[j] = fmaf(w, op[p * D + lane + 32 * j], acc[j]);
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // (NaN stays NaN)
 #pragma unroll
   for (int j = 0; j < PER; ++j) store_out(QF{}, a.out, row * D + lane + 32 * j, acc[j] * inv);
 }
