@@ -1168,7 +1168,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
           const float2 t = dup_ml[srow];
           if (t.y < 0.f) {
             ok = false;  // the other copy gave up: the row's result is lost
-          } else if (ok && t.y > 0.f) {
+          } else if (ok && t.y != 0.f) {  // (0: that copy saw nothing; NaN goes in)
             const float mm = fmaxf(m_used, t.x);
             fa = m_used == -CUDART_INF_F ? 0.f : tc::ex2(m_used - mm);
             fb = tc::ex2(t.x - mm);
@@ -1196,7 +1196,9 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // a split key range, (max, sum) and O / l in fp32 for the combine
       // kernel (a row that sees none of the part's tokens leaves -inf, 0, 0)
       tc::fence_after_sync();
-      const float inv = (l > 0.f ? 1.f / l : 0.f) * (FP8 ? a.v_scale[kvh] : 1.f);
+      // a row that sees nothing is 0; a NaN sum makes it NaN, also where only
+      // the other copy of a row held twice has it
+      const float inv = (l == 0.f ? 0.f : 1.f / l) * (FP8 ? a.v_scale[kvh] : 1.f);
       // MXFP4, bf16 query: V's reference, after the division (together they
       // may leave fp32's range)
       const float vref = MX && C::OBF ? ldexpf(1.f, max(ref_v - kMxTrueRef, -126)) : 1.f;

@@ -143,3 +143,34 @@ def test_split_key_range_keeps_nan(cache, qdt, group, D, qlen):
     # keys in the first, a middle and the last part, the last ones masked from some rows
     check_nan_keys_values_queries(call, [0], [3, 650, 1299 - qlen // 2, 1299])
     check_nan_keys_values_queries(call, [1], [40, 599])
+
+
+# ------------------------------------------------------------- rows held twice
+
+@pytest.mark.parametrize("cache,qdt,group,D,n,qlen", [
+    ("mxfp4", "f16", 1, 128, 3, 8), ("mxfp4", "bf16", 8, 128, 80, 8), ("mxfp4", "bf16", 4, 64, 2, 1),
+    ("mxfp4", "f16", 2, 64, 3, 32), ("f16", "f16", 8, 128, 150, 8), ("bf16", "bf16", 4, 64, 150, 16),
+    ("e4m3", "bf16", 8, 128, 150, 8)])
+@pytest.mark.parametrize("ctx", [90, 700])
+def test_rows_held_twice_keep_nan(cache, qdt, group, D, n, qlen, ctx):
+    """Units of at most 64 rows: each row is in two lanes, for the lower and the upper 32 tokens
+    of every step. NaN keys in either, in the first step, a later one and the last."""
+    call = Call(cache, qdt, [qlen] * n, [ctx] * n, 2, group, D, 16, seed=ctx + n)
+    assert qlen * group <= 64
+    if n > 3:
+        assert not call.split()
+    check_nan_keys_values_queries(call, [n - 1], [5, 40, ctx - 33, ctx - 1])
+
+
+@pytest.mark.parametrize("cache,qdt,Hkv,D,qlens,ctxs", [
+    ("mxfp4", "f16", 2, 128, [100, 70], [300, 160]),                   # one row group
+    ("mxfp4", "bf16", 2, 64, [100, 300], [120, 400]),
+    ("mxfp4", "f16", 40, 64, [260, 130], [4150, 300]),                 # two row groups
+    ("mxfp4", "bf16", 40, 128, [260, 130], [4150, 300]),
+    ("f16", "f16", 2, 128, [300, 270], [400, 300]), ("bf16", "bf16", 2, 64, [130, 70], [300, 90]),
+    ("e4m3", "bf16", 2, 128, [300, 270], [400, 300]), ("bf16", "bf16", 2, 128, [9, 3], [300, 90])])
+def test_whole_key_range_keeps_nan(cache, qdt, Hkv, D, qlens, ctxs):
+    call = Call(cache, qdt, qlens, ctxs, Hkv, 1, D, 16, seed=ctxs[0])
+    assert not call.split()
+    check_nan_keys_values_queries(call, [0], [5, ctxs[0] - 40, ctxs[0] - 1])
+    check_nan_keys_values_queries(call, [1], [2, ctxs[1] - 1])
