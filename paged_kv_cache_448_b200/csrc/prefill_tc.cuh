@@ -67,6 +67,7 @@
 // tensor memory is freed, and the failure is recorded in the error word.
 #pragma once
 
+#include <float.h>
 #include <math_constants.h>
 
 #include <atomic>
@@ -586,9 +587,13 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  // (the exponents together: each alone may leave fp32's range)
+  // (the exponents together: each alone may leave fp32's range. The result is
+  // kept a positive finite number: a masked logit, -inf, times 0 would be NaN,
+  // and so would a product of 0 times infinity. Where the lower bound acts the
+  // logits, with |S| below 2^40, are 0 in either case.)
   if constexpr (MX && C::OBF)
-    if (warp < kMma) qscale = ldexpf(qscale, ref_k - kMxTrueRef - q_exp[tid]);
+    if (warp < kMma)
+      qscale = fminf(fmaxf(ldexpf(qscale, ref_k - kMxTrueRef - q_exp[tid]), FLT_MIN), FLT_MAX);
 
   if (MX && warp >= kLoader) {
     if constexpr (MX) {

@@ -1,0 +1,109 @@
+"""Attention over a 4-bit (MXFP4) cache at the ends of the format: keys that are all zero,
+caches never written, scale bytes at both ends of their range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_ref as mx
+import paged_kv_cache_448_b200 as pk
+from gpu_helpers import Guarded, guarded_workspace, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def chunk(q, planes, table, ctxs, qlens, scale):
+    T, H, D = q.shape
+    Hkv = planes[0].shape[1]
+    out = Guarded(tuple(q.shape), q.dtype, fill=5.0)
+    ws = guarded_workspace(pk.chunked_prefill_workspace_size(
+        len(qlens), T, H, Hkv, D, max(qlens), max(ctxs), pk.PA_MXFP4))
+    cu = i32(np.concatenate([[0], np.cumsum(qlens)]))
+    pk.chunked_prefill_mxfp4(out.t, q, cu, max(qlens), *planes, i32(table), i32(ctxs), max(ctxs),
+                             scale, workspace=ws.t)
+    torch.cuda.synchronize()
+    out.check("output"), ws.check("workspace")
+    pk.decode_check(ws.t)
+    return out.t
+
+
+def decode(q, planes, table, ctxs, scale, partition=0):
+    S, H, D = q.shape
+    Hkv, bs = planes[0].shape[1:3]
+    out = Guarded(tuple(q.shape), q.dtype, fill=5.0)
+    ws = guarded_workspace(pk.decode_workspace_size(S, H, Hkv, D, bs, max(ctxs), partition,
+                                                    pk.PA_MXFP4))
+    pk.decode_mxfp4(out.t, q, *planes, i32(table), i32(ctxs), max(ctxs), scale,
+                    partition_tokens=partition, workspace=ws.t)
+    torch.cuda.synchronize()
+    out.check("output"), ws.check("workspace")
+    pk.decode_check(ws.t)
+    return out.t
+
+
+# ------------------------------------------------------------- keys of zero
+
+UNITS = {  # query lengths, contexts, query heads on one kv-head
+    "doubled": ([8, 3], [300, 40], 8), "one group": ([100, 60], [300, 160], 1),
+    "split": ([100], [1100], 1), "split, doubled": ([6], [900], 2)}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("byte", [0, 1])
+@pytest.mark.parametrize("units", list(UNITS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_of_zero_give_the_mean(dtype, byte, units, D):
+    """Keys of zero (rows of zeros are written with scale byte 1, a new cache has byte 0): every
+    visible token weighs the same, whatever the query, down to its type's smallest number."""
+    qlens, ctxs, group = UNITS[units]
+    rng = np.random.default_rng(41)
+    cache = mx.Cache(ctxs, 1, D, 16, rng)
+    cache.kc[:] = 0
+    cache.ks[:] = np.where(cache.ks == 255, 255, byte)
+    planes = [mx.to_dev(p) for p in cache.planes]
+    tiny = torch.finfo(mx.TORCH[dtype]).smallest_normal
+    for amp in (1.0, 2.0 ** -12, tiny, tiny * torch.finfo(mx.TORCH[dtype]).eps, 0.0):
+        for scale in (1 / math.sqrt(D), -1e-3):
+            q, qx = mx.query(rng, sum(qlens), group, D, dtype, amp)
+            ref, bound = mx.attention(qx, cache, qlens, scale, dtype)
+            mx.check(chunk(q, planes, cache.table, ctxs, qlens, scale), ref, bound,
+                     f"chunks, query {amp}")
+            one = q[:len(ctxs)].contiguous()
+            ref, bound = mx.attention(qx[:len(ctxs)], cache, [1] * len(ctxs), scale, dtype)
+            mx.check(decode(one, planes, cache.table, ctxs, scale), ref, bound,
+                     f"decode, query {amp}")
+
+
+def test_two_row_groups_over_keys_of_zero():
+    Hkv, qlens, ctxs = 40, [260, 130], [4150, 300]
+    planes = pk.mxfp4_cache(300, Hkv, 16, 64)
+    v = torch.randn(4800, Hkv, 64, device="cuda").to(torch.bfloat16)
+    pk.reshape_and_cache_mxfp4(torch.zeros_like(v), v, *planes, i32(np.arange(4800)))
+    back, value = torch.empty_like(v), torch.empty_like(v)
+    pk.gather_cache_mxfp4(back, value, *planes, i32(np.arange(4800)))
+    table = np.full((2, 260), -1, np.int32)
+    table[0], table[1, :19] = np.arange(260), np.arange(260, 279)
+    q = torch.full((390, Hkv, 64), 2.0 ** -12, device="cuda", dtype=torch.bfloat16)
+    out = chunk(q, planes, table, ctxs, qlens, 0.125)
+    at = 0
+    for s, n in enumerate(qlens):
+        x = value[4160 * s:4160 * s + ctxs[s]].double()
+        count = torch.arange(1, ctxs[s] + 1, device="cuda", dtype=torch.float64)[:, None, None]
+        mean, size = (y.cumsum(0) / count for y in (x, x.abs()))
+        ref = mean[ctxs[s] - n:]
+        # the output's rounding; 2^-11 a probability in f16; 2^-13 sums in fp32 (as in mxfp4_ref)
+        bound = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -13) * size[ctxs[s] - n:] + \
+            ctxs[s] * 2.0 ** -24 * x.abs().amax(0)
+        assert ((out[at:at + n].double() - ref).abs() <= bound).all()
+        at += n
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_cache_never_written(dtype):
+    planes = pk.mxfp4_cache(80, 2, 16, 128)
+    for qlens, ctxs in (([8, 3], [300, 40]), ([100, 60], [300, 160]), ([100], [1100])):
+        table = np.arange(len(ctxs) * 69).reshape(len(ctxs), 69) % 80
+        q = torch.randn(sum(qlens), 4, 128, device="cuda").mul(2.0 ** -9).to(mx.TORCH[dtype])
+        assert not chunk(q, planes, table, ctxs, qlens, 0.09).any()
+        assert not decode(q[:len(ctxs)].contiguous(), planes, table, ctxs, 0.09).any()
