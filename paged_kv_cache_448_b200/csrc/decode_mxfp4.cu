@@ -376,8 +376,8 @@ struct MxState {
           for (int j = 0; j < 2; ++j)
             if (16 * u + 8 * i + 2 * c + j >= valid) vw[u][i][j] = in;
     }
-    const bool lift =
-        mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || outside(vw) || ff;
+    const bool lift = mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || outside(vw) || ff ||
+                      (low && far_above(vw));
     bool wide = low;  // V scales below the window (the same in every lane)
     if (__any_sync(FULL, lift)) {
       update(x, mx, kw, ff, vw);
@@ -434,8 +434,11 @@ struct MxState {
   }
 
   // Nonzero if some V scale of the step is not within [r_b - 8, r_b + 7] of its
-  // block's reference: whole words of scales at once (w + off has an upper
-  // nibble of 8 in every byte exactly when every byte is within its window).
+  // block's reference: whole words of scales at once. w + off has an upper
+  // nibble of 8 in every byte when every byte is within its window, and not in
+  // the lowest one that is outside it, but for a byte so far above that the sum
+  // runs through to the nibble again: r_b + 248 and more. Those need r_b <= 7
+  // (low is set then) and are what far_above finds.
   __device__ __forceinline__ uint32_t outside(const uint32_t (&vw)[2][2][2]) const {
     uint32_t bits = 0u;
 #pragma unroll
@@ -445,6 +448,18 @@ struct MxState {
 #pragma unroll
         for (int j = 0; j < 2; ++j) bits |= (vw[u][i][j] + off) ^ 0x80808080u;
     return bits & (NB == 4 ? 0xf0f0f0f0u : 0x0000f0f0u);
+  }
+
+  // Nonzero if some V scale of the step is 248 or more (NaN, 255, among them).
+  static __device__ __forceinline__ uint32_t far_above(const uint32_t (&vw)[2][2][2]) {
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) bits |= has_ff(vw[u][i][j] | 0x07070707u);
+    return bits;
   }
 
   // The V scales of block b of two tokens (words w) as halves.

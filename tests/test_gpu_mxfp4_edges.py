@@ -107,3 +107,41 @@ def test_a_cache_never_written(dtype):
         q = torch.randn(sum(qlens), 4, 128, device="cuda").mul(2.0 ** -9).to(mx.TORCH[dtype])
         assert not chunk(q, planes, table, ctxs, qlens, 0.09).any()
         assert not decode(q[:len(ctxs)].contiguous(), planes, table, ctxs, 0.09).any()
+
+
+# ------------------------------------------------------------- values of zero, then a far scale
+
+@pytest.mark.parametrize("Hkv,group,D,dtype", [
+    (1, 8, 128, "bf16"), (2, 4, 128, "f16"), (1, 8, 64, "bf16"), (2, 2, 128, "bf16"),
+    (1, 1, 64, "f16")])
+@pytest.mark.parametrize("zero", [0, 1, 6])
+def test_far_value_scales_after_values_of_zero(Hkv, group, D, dtype, zero):
+    """All logits alike, so that no maximum moves; values of zero (scale bytes as a new cache and
+    the writer leave them, and a larger one), and in a later step of the same warp a block of NaN
+    or one of the largest scales."""
+    rng = np.random.default_rng(42)
+    ctxs = [300, 70]
+    for far in (255, 254, 250, 248 + zero, 247):
+        for at in (130, 159, 261, 299):
+            cache = mx.Cache(ctxs, Hkv, D, 16, rng)
+            cache.kc[:] = 0
+            cache.vc[:] = 0
+            for plane in (cache.ks, cache.vs):
+                plane[:] = np.where(plane == 255, 255, zero)
+            blk = at % (D // 32)
+            where = (int(cache.table[0, at // 16]), Hkv - 1, at % 16)
+            cache.vs[where + (blk,)] = far
+            cache.vc[where + (slice(16 * blk, 16 * blk + 16),)] = 0x21        # 0.5 and 1
+            planes = [mx.to_dev(p) for p in cache.planes]
+            q, qx = mx.query(rng, 2, Hkv * group, D, dtype)
+            out = decode(q, planes, cache.table, ctxs, 0.1, partition=512)
+            mine = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+            mine[0, -group:, 32 * blk:32 * blk + 32] = True
+            assert not out[~mine].any()
+            if far == 255:
+                assert torch.isnan(out[mine]).all()
+            elif dtype == "f16":
+                assert torch.isinf(out[mine]).all()
+            else:
+                ref, bound = mx.attention(qx, cache, [1, 1], 0.1, dtype)
+                mx.check(out, ref, bound, f"scale byte {far}")
