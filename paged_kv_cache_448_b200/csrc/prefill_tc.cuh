@@ -1204,9 +1204,10 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // a row that sees nothing is 0; a NaN sum makes it NaN, also where only
       // the other copy of a row held twice has it
       const float inv = (l == 0.f ? 0.f : 1.f / l) * (FP8 ? a.v_scale[kvh] : 1.f);
-      // MXFP4, bf16 query: V's reference, after the division (together they
-      // may leave fp32's range)
-      const float vref = MX && C::OBF ? ldexpf(1.f, max(ref_v - kMxTrueRef, -126)) : 1.f;
+      // MXFP4, bf16 query: V's reference (2^-140 .. 2^114, below 2^-126 an fp32
+      // subnormal number), after the division (together they may leave fp32's
+      // range)
+      const float vref = MX && C::OBF ? ldexpf(1.f, ref_v - kMxTrueRef) : 1.f;
       auto res = [&](float x) {
         if constexpr (MX && C::OBF) return x * inv * vref;
         else return x * inv;

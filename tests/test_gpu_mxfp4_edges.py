@@ -145,3 +145,23 @@ def test_far_value_scales_after_values_of_zero(Hkv, group, D, dtype, zero):
             else:
                 ref, bound = mx.attention(qx, cache, [1, 1], 0.1, dtype)
                 mx.check(out, ref, bound, f"scale byte {far}")
+
+
+# ------------------------------------------------------------- the smallest and largest values
+
+@pytest.mark.parametrize("units", list(UNITS))
+@pytest.mark.parametrize("e", [-125, -122, -118, -115, -112, -60, 100])
+def test_values_of_every_size(units, e):
+    """Values around 2^e, bf16 (its normal numbers go down to 2^-126)."""
+    qlens, ctxs, group = UNITS[units]
+    rng = np.random.default_rng(43)
+    cache = mx.Cache(ctxs, 1, 128, 16, rng, v_rows=lambda s: rng.standard_normal(s) * 2.0 ** e)
+    planes = [mx.to_dev(p) for p in cache.planes]
+    q, qx = mx.query(rng, sum(qlens), group, 128, "bf16")
+    # the output and the sums are off by half a step of bf16's and fp32's smallest numbers as well
+    extra = 2.0 ** -134 + max(ctxs) * 2.0 ** -149
+    ref, bound = mx.attention(qx, cache, qlens, 0.1, "bf16")
+    mx.check(chunk(q, planes, cache.table, ctxs, qlens, 0.1), ref, bound + extra, "chunks")
+    ref, bound = mx.attention(qx[:len(ctxs)], cache, [1] * len(ctxs), 0.1, "bf16")
+    mx.check(decode(q[:len(ctxs)].contiguous(), planes, cache.table, ctxs, 0.1), ref,
+             bound + extra, "decode")
