@@ -418,14 +418,15 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
 /*
  * pa_chunked_prefill over an MXFP4 cache: the same operation, arguments, limits,
  * workspace (pa_chunked_prefill_workspace_size with PA_MXFP4) and run-time
- * table errors; q_dtype F16 or BF16. Keys and values enter the products in F16:
- * with an F16 query as they are, scales of more than 2^13 (b > 140) taken as
- * 2^13 and those below 2^-24 (b < 103) as 0 (exact for caches written from F16
- * rows but for codes below F16's own resolution); with a BF16 query relative
- * to the largest scale among the keys (values) that a work unit reads, exact
- * down to 2^-36 of it, with an error of at most 2^-38 of the largest magnitude
- * below. A NaN block makes NaN what it belongs to (a V block: its 32 outputs)
- * in every row of a tile of query rows that reads it, masked or not.
+ * table errors; q_dtype F16 or BF16. Keys and values enter the products in F16,
+ * relative to the largest scale among the keys (values) that a work unit reads:
+ * exact down to 2^-36 of it, with an error of at most 2^-38 of the largest
+ * magnitude below. With an F16 query a V block whose scale is more than 2^13
+ * (b > 140; no F16 row gives one, a BF16 row of values from 2^16 does) is read
+ * with the scale 2^13, where pa_decode_mxfp4 and pa_gather_cache_mxfp4 read it
+ * as it is. A NaN block of K makes NaN every output row that attends to it, one
+ * of V its 32 outputs in those rows, and perhaps also in rows of the same tile
+ * of query rows (at most 256) from which it is masked.
  */
 PA_API pa_status pa_chunked_prefill_mxfp4(
     void* out, const void* query, const int32_t* cu_query_lens, int32_t num_tokens,

@@ -307,7 +307,9 @@ def chunked_prefill_mxfp4(out, query, cu_query_lens, max_query_len: int, key_cac
                           scale: float, *, workspace=None, stream=None):
     """chunked_prefill over an MXFP4 cache (pa_chunked_prefill_mxfp4): out/query [T, H, D]
     f16|bf16, planes as mxfp4_cache makes them; workspace from
-    chunked_prefill_workspace(..., PA_MXFP4). Returns ``out``."""
+    chunked_prefill_workspace(..., PA_MXFP4). With an f16 query, V blocks whose scale is
+    above 2^13 (values from 2^16, which only bf16 rows have) read as with 2^13.
+    Returns ``out``."""
     if workspace is None:
         T, H, D = query.shape
         workspace = _own_workspace(query, stream, lambda: chunked_prefill_workspace(

@@ -50,10 +50,14 @@
 // completed they write
 // code * 2^(b - r + 13) into it in the layout the TMA boxes have. From there on
 // it is the f16 kernel. r is a reference for the scales, undone in the logit
-// scale and the epilogue: with an f16 query 140 (the values themselves), with a
-// bf16 query the largest scale byte among the CTA's keys (values), so that
-// every value down to 2^-36 of the largest is exact in f16; it is found by
-// reading the scale bytes once before the pipeline starts. (Widening to bf16
+// scale and the epilogue: the largest scale byte among the CTA's keys (values),
+// so that every value down to 2^-36 of the largest is exact in f16; it is found
+// by reading the scale bytes once before the pipeline starts. With an f16 query
+// V's reference is 140 at most: a block of a larger scale, which no f16 row
+// gives, reads as with 2^13. (References of 140 throughout would spare an f16
+// query the pass over the scale bytes, 512-token chunks of 32 heads 208 us
+// against 227, but read keys beyond f16's range, and blocks of its smallest
+// numbers, as others than decode does.) (Widening to bf16
 // needs no reference, but three times the instructions of the conversion to
 // f16, which are what bounds the kernel, and P in two parts: 8 draft tokens x
 // 8 heads of 64 sequences took 202 us.) A bf16 query row is scaled by a power
@@ -265,7 +269,8 @@ constexpr int kMxTrueRef = 140;
 
 // 32 codes of one block and their scale byte b <= r -> f16 of code * 2^(b - r + 13)
 // (nearest), four 16-byte chunks of 8 dims. Scales above the reference are
-// taken as the reference (no product overflows), a byte of 0 reads as 0.
+// taken as the reference (no product overflows), a byte of 0 reads as 0, and so
+// do scales more than 2^37 below the reference.
 __device__ __forceinline__ void mx_widen(const uint4& codes, int b, int r, uint4 (&out)[4]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   const int field = min(b, r) - r + 28;  // f16 exponent field of the factor
@@ -442,23 +447,28 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     }
   }
 
-  // MXFP4, bf16 query: the largest scale bytes of this CTA's keys and values
+  // MXFP4: the largest scale bytes of this CTA's keys and values
   // (255, a NaN block, aside; bytes of rows that are not there do not count)
   __shared__ int ref_part[2][C::THREADS / 32];
-  if constexpr (MX && C::OBF) {
+  if constexpr (MX) {
     const int kv_end = min(ctx, tend * TR);
     const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
     const int bs_log = a.block_size == 32 ? 5 : 4;
     // 16 bytes of scales a thread and load (VT tokens of one block), several
     // loads of block ids, then of scales, in flight
     constexpr int NB = D / 32, VT = 16 / NB, BATCH = 3;
+    // a byte counts as byte + 1, a NaN's 255 and a missing row's as 0; two bytes
+    // a word, in halves
     uint32_t top[2] = {0u, 0u};
+    auto counted = [](uint32_t x) { return ((x & 0x00ff00ffu) + 0x00010001u) & 0x00ff00ffu; };
     for (int t0 = tbase * TR + tid * VT; t0 < kv_end; t0 += BATCH * C::THREADS * VT) {
       int32_t id[BATCH];
       uint4 w[BATCH][2];
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j)
-        id[j] = table[min(t0 + j * C::THREADS * VT, kv_end - 1) >> bs_log];
+      for (int j = 0; j < BATCH; ++j) {
+        const int t = t0 + j * C::THREADS * VT;
+        id[j] = t < kv_end ? table[t >> bs_log] : -1;
+      }
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {
         const bool known = static_cast<uint32_t>(id[j]) < static_cast<uint32_t>(a.num_blocks);
@@ -467,7 +477,8 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
                                 a.block_size + (t & (a.block_size - 1));
 #pragma unroll
         for (int v = 0; v < 2; ++v)
-          w[j][v] = __ldcg(reinterpret_cast<const uint4*>(cache.scales[v] + row * NB));
+          w[j][v] = known ? __ldcg(reinterpret_cast<const uint4*>(cache.scales[v] + row * NB))
+                          : make_uint4(0u, 0u, 0u, 0u);
         if (!known) id[j] = -1;
       }
 #pragma unroll
@@ -477,28 +488,31 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
         for (int v = 0; v < 2; ++v) {
           const uint32_t x[4] = {w[j][v].x, w[j][v].y, w[j][v].z, w[j][v].w};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t b = (x[i / 4] >> (8 * (i % 4))) & 255u;
-            if (i / NB < rows && b != kMxNan) top[v] = max(top[v], b);
+          for (int i = 0; i < 4; ++i) {
+            constexpr int RW = 4 / NB;  // rows of a word
+            uint32_t y = x[i];
+            if (RW == 2 && RW * i + 1 >= rows) y |= 0xffff0000u;
+            if (RW * i >= rows) y = 0xffffffffu;
+            top[v] = __vmaxu2(top[v], __vmaxu2(counted(y), counted(y >> 8)));
           }
         }
       }
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      top[v] = __reduce_max_sync(0xffffffffu, top[v]);
-      if (lane == 0) ref_part[v][warp] = static_cast<int>(top[v]);
+      const uint32_t t = __reduce_max_sync(0xffffffffu, max(top[v] & 0xffffu, top[v] >> 16));
+      if (lane == 0) ref_part[v][warp] = max(static_cast<int>(t) - 1, 0);
     }
   }
   __syncthreads();  // barrier initialisation visible to every thread
-  int ref_k = kMxTrueRef, ref_v = kMxTrueRef;
-  if constexpr (MX && C::OBF) {
-    ref_k = ref_v = 0;
+  int ref_k = 0, ref_v = 0;
+  if constexpr (MX) {
 #pragma unroll
     for (int i = 0; i < C::THREADS / 32; ++i) {
       ref_k = max(ref_k, ref_part[0][i]);
       ref_v = max(ref_v, ref_part[1][i]);
     }
+    if (!C::OBF) ref_v = min(ref_v, kMxTrueRef);
   }
   if (warp == kMma) tc::alloc(&tmem_slot, C::TMEM_COLS);
   if constexpr (!FP8) {
@@ -591,9 +605,11 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
   // kept a positive finite number: a masked logit, -inf, times 0 would be NaN,
   // and so would a product of 0 times infinity. Where the lower bound acts the
   // logits, with |S| below 2^40, are 0 in either case.)
-  if constexpr (MX && C::OBF)
-    if (warp < kMma)
-      qscale = fminf(fmaxf(ldexpf(qscale, ref_k - kMxTrueRef - q_exp[tid]), FLT_MIN), FLT_MAX);
+  if constexpr (MX)
+    if (warp < kMma) {
+      const int e = ref_k - kMxTrueRef - (C::OBF ? q_exp[tid] : 0);
+      qscale = fminf(fmaxf(ldexpf(qscale, e), FLT_MIN), FLT_MAX);
+    }
 
   if (MX && warp >= kLoader) {
     if constexpr (MX) {
@@ -1204,12 +1220,11 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // a row that sees nothing is 0; a NaN sum makes it NaN, also where only
       // the other copy of a row held twice has it
       const float inv = (l == 0.f ? 0.f : 1.f / l) * (FP8 ? a.v_scale[kvh] : 1.f);
-      // MXFP4, bf16 query: V's reference (2^-140 .. 2^114, below 2^-126 an fp32
-      // subnormal number), after the division (together they may leave fp32's
-      // range)
-      const float vref = MX && C::OBF ? ldexpf(1.f, ref_v - kMxTrueRef) : 1.f;
+      // MXFP4: V's reference (2^-140 .. 2^114, below 2^-126 an fp32 subnormal
+      // number), after the division (together they may leave fp32's range)
+      const float vref = MX ? ldexpf(1.f, ref_v - kMxTrueRef) : 1.f;
       auto res = [&](float x) {
-        if constexpr (MX && C::OBF) return x * inv * vref;
+        if constexpr (MX) return x * inv * vref;
         else return x * inv;
       };
       if (parts == 1) {

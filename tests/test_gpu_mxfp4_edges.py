@@ -165,3 +165,38 @@ def test_values_of_every_size(units, e):
     ref, bound = mx.attention(qx[:len(ctxs)], cache, [1] * len(ctxs), 0.1, "bf16")
     mx.check(decode(q[:len(ctxs)].contiguous(), planes, cache.table, ctxs, 0.1), ref,
              bound + extra, "decode")
+
+
+@pytest.mark.parametrize("units", list(UNITS))
+@pytest.mark.parametrize("k,v", [(-60, 0), (-24, -20), (0, -23), (20, -10), (60, 8), (14, 13)])
+def test_f16_query_over_scales_that_f16_rows_do_not_have(units, k, v):
+    """Keys around 2^k (the softmax scale makes up for it) and values around 2^v, as bf16 rows
+    write them: both calls read the same cache."""
+    qlens, ctxs, group = UNITS[units]
+    rng = np.random.default_rng(44)
+    cache = mx.Cache(ctxs, 1, 64, 32, rng, k_rows=lambda s: rng.standard_normal(s) * 2.0 ** k,
+                     v_rows=lambda s: np.clip(rng.standard_normal(s), -3.9, 3.9) * 2.0 ** v)
+    assert cache.vs[cache.vs < 255].max() <= 140
+    planes = [mx.to_dev(p) for p in cache.planes]
+    q, qx = mx.query(rng, sum(qlens), group, 64, "f16", amp=3.0)
+    scale = 0.1 * 2.0 ** -k
+    extra = 2.0 ** -25                                   # half of f16's smallest step
+    ref, bound = mx.attention(qx, cache, qlens, scale, "f16")
+    mx.check(chunk(q, planes, cache.table, ctxs, qlens, scale), ref, bound + extra, "chunks")
+    ref, bound = mx.attention(qx[:len(ctxs)], cache, [1] * len(ctxs), scale, "f16")
+    mx.check(decode(q[:len(ctxs)].contiguous(), planes, cache.table, ctxs, scale), ref,
+             bound + extra, "decode")
+
+
+def test_blocks_of_f16s_smallest_numbers():
+    """Values of a few times 2^-24 (scale bytes 101 and 102) are f16 numbers and read as such."""
+    D = 64
+    v = torch.full((16, 1, D), 2.0 ** -24, device="cuda").half()
+    v[:, :, 32:] = 3 * 2.0 ** -24
+    planes = pk.mxfp4_cache(1, 1, 16, D)
+    pk.reshape_and_cache_mxfp4(v, v, *planes, i32(np.arange(16)))
+    assert set(planes[3].flatten().tolist()) == {101, 102}
+    q = torch.randn(12, 1, D, device="cuda").half()
+    out = chunk(q, planes, [[0]], [16], [12], 0.1)
+    assert torch.equal(out, v[:12])
+    assert torch.equal(decode(q[:1].contiguous(), planes, [[0]], [16], 0.1), v[:1])
