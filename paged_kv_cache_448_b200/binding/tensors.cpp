@@ -125,8 +125,18 @@ double number(PyObject* o, const char* name) {
   return v;
 }
 
-// call(stream) with device dev current; stream None: the device's current one,
-// else the handle (an integer).
+// Other Python threads run while this lives: a launch waits for room in the
+// GPU's queue, and what empties the queue may need them (a host callback).
+struct WithoutLock {
+  PyThreadState* state = PyEval_SaveThread();
+  WithoutLock() = default;
+  WithoutLock(const WithoutLock&) = delete;
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+
+// call(stream) with device dev current and the interpreter lock released (call
+// touches no Python object); stream None: the device's current one, else the
+// handle (an integer).
 template <class F>
 PyObject* launch(int dev, PyObject* stream, F call) {
   if (dev < 0) bad("tensors must be on a CUDA device");
@@ -139,7 +149,12 @@ PyObject* launch(int dev, PyObject* stream, F call) {
     PyErr_Clear();
     throw TypeProblem("stream must be a CUDA stream");
   }
-  return PyLong_FromLong(call(static_cast<pa_stream_t>(handle)));
+  long status;
+  {
+    const WithoutLock unlocked;
+    status = call(static_cast<pa_stream_t>(handle));
+  }
+  return PyLong_FromLong(status);
 }
 
 template <class F>
