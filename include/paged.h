@@ -469,10 +469,9 @@ typedef struct pa_plane {
  * context_lens      device int32 [num_seqs]
  * parents, fresh_blocks  device int32 [num_children]; a parent may be named
  *                   many times; the fresh blocks are distinct and no parent's.
- * new_block_tables  device int32 [num_children, max_blocks_per_seq] (written;
- *                   does not overlap block_tables)
- * new_context_lens  device int32 [num_children] (written; no overlap with
- *                   context_lens)
+ * new_block_tables  device int32 [num_children, max_blocks_per_seq] (written)
+ * new_context_lens  device int32 [num_children] (written; neither overlaps an
+ *                   input or the other: PA_ERR_INVALID_ARG)
  * error_word        optional device int32: bit 32 is set for a parent that is
  *                   no sequence (its child gets length 0 and no blocks), bit 1
  *                   for a block id outside the pool (nothing is copied; a fresh
@@ -495,7 +494,8 @@ PA_API pa_status pa_fork_sequences(const pa_plane* planes, int32_t num_planes, i
  * distinct and none of them is a source (pa_alloc_compact makes such a list);
  * entries that name no moved block stay as they are, -1 included.
  * moves             device int32 [num_moves][2]
- * block_tables      device int32, num_entries entries in all (or NULL and 0)
+ * block_tables      device int32, num_entries entries in all (or NULL and 0); does
+ *                   not overlap moves (PA_ERR_INVALID_ARG)
  * error_word        optional device int32: bit 1 is set for a move with an id
  *                   outside the pool (it is left out, entries too), bit 64 for
  *                   sources that do not ascend or a destination that is a

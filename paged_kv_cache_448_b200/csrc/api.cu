@@ -980,10 +980,17 @@ PA_API pa_status pa_fork_sequences(const pa_plane* planes, int32_t num_planes, i
       !aligned(fresh_blocks, 4) || !aligned(new_block_tables, 4) ||
       !aligned(new_context_lens, 4) || !aligned(error_word, 4))
     return fail(PA_ERR_INVALID_ARG, "fork_sequences: misaligned pointer");
+  // one warp writes a child's row and length while others still read the inputs
   const int64_t row = 4LL * max_blocks_per_seq, n = num_children;
-  if (overlap(block_tables, row * num_seqs, new_block_tables, row * n) ||
-      overlap(context_lens, 4LL * num_seqs, new_context_lens, 4 * n))
-    return fail(PA_ERR_INVALID_ARG, "fork_sequences: the new tables overlap the old ones");
+  auto over_inputs = [&](const int32_t* p, int64_t bytes) {
+    return overlap(p, bytes, block_tables, row * num_seqs) ||
+           overlap(p, bytes, context_lens, 4LL * num_seqs) || overlap(p, bytes, parents, 4 * n) ||
+           overlap(p, bytes, fresh_blocks, 4 * n);
+  };
+  if (over_inputs(new_block_tables, row * n) || over_inputs(new_context_lens, 4 * n) ||
+      overlap(new_block_tables, row * n, new_context_lens, 4 * n))
+    return fail(PA_ERR_INVALID_ARG,
+                "fork_sequences: the new tables overlap the inputs or one another");
   ForkArgs a{};
   a.block_tables = block_tables;
   a.context_lens = context_lens;
@@ -1016,6 +1023,8 @@ PA_API pa_status pa_compact_blocks(const pa_plane* planes, int32_t num_planes, i
     return fail(PA_ERR_INVALID_ARG, "compact_blocks: null pointer");
   if (!aligned(moves, 8) || !aligned(block_tables, 4) || !aligned(error_word, 4))
     return fail(PA_ERR_INVALID_ARG, "compact_blocks: misaligned pointer");
+  if (num_entries > 0 && overlap(block_tables, 4 * num_entries, moves, 8LL * num_moves))
+    return fail(PA_ERR_INVALID_ARG, "compact_blocks: the table overlaps the moves");
   CompactArgs a{};
   a.moves = moves;
   a.block_tables = block_tables;
