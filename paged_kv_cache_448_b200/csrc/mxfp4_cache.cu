@@ -156,7 +156,6 @@ __global__ void __launch_bounds__(kThreads)
                       const uint32_t* __restrict__ kc, const uint32_t* __restrict__ vc,
                       const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
                       const RowArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int CPR = D / 8;
   const uint32_t i0 = blockIdx.x * (kThreads * kReadChunks) + threadIdx.x;
   uint32_t kw[kReadChunks], vw[kReadChunks];

@@ -1151,7 +1151,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
               make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      fence_proxy_async_smem();
+      if constexpr (!MX) fence_proxy_async_smem();  // the cleared rows above
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_bar[g][k & 1]);
