@@ -1099,8 +1099,10 @@ __global__ void __launch_bounds__(NW * 32, 4)
       // NaN logits has m = -inf and l = NaN, which must survive
       const float f = mw == -CUDART_INF_F ? (lw == 0.f ? 0.f : 1.f) : exp2f(mw - M);
       L += lw * f;
-      const float v = obuf[(w * 8 + h) * D + d];  // (not written by a warp without steps)
-      o = f != 0.f ? fmaf(v, f, o) : o;
+      // not written by a warp without steps; a NaN block of V counts whatever
+      // its weight, so a weight that underflowed to 0 is multiplied all the same
+      const float v = obuf[(w * 8 + h) * D + d];
+      o = lw != 0.f ? fmaf(v, f, o) : o;
     }
     o = L == 0.f ? 0.f : o / L;
     if (single) {

@@ -200,3 +200,34 @@ def test_blocks_of_f16s_smallest_numbers():
     out = chunk(q, planes, [[0]], [16], [12], 0.1)
     assert torch.equal(out, v[:12])
     assert torch.equal(decode(q[:1].contiguous(), planes, [[0]], [16], 0.1), v[:1])
+
+
+# ------------------------------------------------------------- NaN values without weight
+
+@pytest.mark.parametrize("Hkv,group,D,dtype", [(1, 8, 128, "bf16"), (2, 1, 128, "f16"),
+                                               (1, 4, 64, "bf16"), (1, 2, 64, "f16")])
+@pytest.mark.parametrize("partition", [32, 512])
+def test_a_nan_value_whose_weight_underflows(Hkv, group, D, dtype, partition):
+    """Logits hundreds below the largest have the weight 0 in fp32; a NaN value among them, in any
+    warp, partition or tile, makes its 32 outputs NaN as the formula has it (0 times NaN)."""
+    rng = np.random.default_rng(45)
+    ctxs = [400]
+    cache = mx.Cache(ctxs, Hkv, D, 16, rng, k_rows=lambda s: np.ones(s))
+    top = (int(cache.table[0, 5]), slice(None), 3)             # token 83: the largest logit by far
+    c, sc = mx.encode(np.full((1, D), 6.0))
+    cache.kc[top], cache.ks[top] = c[0], sc[0]
+    q = torch.ones(1, Hkv * group, D, device="cuda").to(mx.TORCH[dtype])
+    scale = 500.0 / (5 * D)                                    # e^-500 for the others
+    clean = [mx.to_dev(p) for p in cache.planes]
+    want = decode(q, clean, cache.table, ctxs, scale, partition)
+    want_chunk = chunk(q, clean, cache.table, ctxs, [1], scale)
+    for t in (0, 40, 70, 82, 84, 200, 399):
+        spoilt = cache.vs.copy()
+        spoilt[int(cache.table[0, t // 16]), 0, t % 16, 1] = 255
+        planes = clean[:3] + [mx.to_dev(spoilt)]
+        bad = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+        bad[:, :group, 32:64] = True
+        out = decode(q, planes, cache.table, ctxs, scale, partition)
+        assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want[~bad]), t
+        out = chunk(q, planes, cache.table, ctxs, [1], scale)
+        assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want_chunk[~bad]), t
