@@ -196,11 +196,6 @@ __device__ __forceinline__ void load_codes(const uint8_t* tile, int u, int lane,
   }
 }
 
-// Nonzero if some byte of w is 255.
-__device__ __forceinline__ uint32_t has_ff(uint32_t w) {
-  return (~w - 0x01010101u) & w & 0x80808080u;
-}
-
 // 16 bytes global -> shared, or 16 zero bytes.
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),

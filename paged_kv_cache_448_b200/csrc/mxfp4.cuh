@@ -43,6 +43,11 @@ __device__ __forceinline__ float mx_scale(int b) {
                      : __uint_as_float(static_cast<uint32_t>(b) << 23);
 }
 
+// Nonzero if some byte of w is 255.
+__device__ __forceinline__ uint32_t has_ff(uint32_t w) {
+  return (~w - 0x01010101u) & w & 0x80808080u;
+}
+
 // Eight scaled values -> eight codes (element 0 in the low half of byte 0),
 // round to nearest even, saturating.
 __device__ __forceinline__ uint32_t mx_pack8(const float (&v)[8]) {

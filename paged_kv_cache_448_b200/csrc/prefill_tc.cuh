@@ -61,8 +61,11 @@
 // needs no reference, but three times the instructions of the conversion to
 // f16, which are what bounds the kernel, and P in two parts: 8 draft tokens x
 // 8 heads of 64 sequences took 202 us.) A bf16 query row is scaled by a power
-// of two that puts its largest element in [1, 2). The warps take the items of K and V in one
-// order, K a step ahead of V; a stage is full when each of its items arrived.
+// of two that puts its largest element in [1, 2). A stage is full when each of
+// its converter warps arrived. NaN blocks go in as zeros, and the pass over the
+// scales keeps the first token that makes a block of the output's dims NaN: in
+// an MMA a NaN of V would reach every row, those from which the causal mask
+// hides it too.
 // The register file is shared out anew once the roles are known (softmax
 // warps more, the others less).
 // Every wait is bounded by wall time. A wait that gives up sets a shared
@@ -72,6 +75,7 @@
 #pragma once
 
 #include <float.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include <atomic>
@@ -270,13 +274,12 @@ constexpr int kMxTrueRef = 140;
 // 32 codes of one block and their scale byte b <= r -> f16 of code * 2^(b - r + 13)
 // (nearest), four 16-byte chunks of 8 dims. Scales above the reference are
 // taken as the reference (no product overflows), a byte of 0 reads as 0, and so
-// do scales more than 2^37 below the reference.
+// do scales more than 2^37 below the reference, and 255 (NaN) too.
 __device__ __forceinline__ void mx_widen(const uint4& codes, int b, int r, uint4 (&out)[4]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   const int field = min(b, r) - r + 28;  // f16 exponent field of the factor
   uint32_t f = field > 0 ? static_cast<uint32_t>(field) << 10 : field > -10 ? 512u >> -field : 0u;
-  if (b == 0) f = 0u;
-  if (b == kMxNan) f = 0x7e00u;
+  if (b == 0 || b == kMxNan) f = 0u;
   f *= 0x10001u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -339,6 +342,13 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t lim = a.wait_limit_ns;
+  // MXFP4: per block of the output's dims, the first of this CTA's tokens that
+  // makes it NaN: a NaN block of V its own, one of K all of them
+  __shared__ int nan_token[MX ? D / 32 : 1];
+  if constexpr (MX) {
+    if (tid < D / 32) nan_token[tid] = INT_MAX;
+    __syncthreads();
+  }
   if (tid == 0) {
     for (int r = 0; r < KR; ++r) {
       mbar_init(&kfull[r], MX ? C::CW : 1);
@@ -457,46 +467,63 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
     // 16 bytes of scales a thread and load (VT tokens of one block), several
     // loads of block ids, then of scales, in flight
     constexpr int NB = D / 32, VT = 16 / NB, BATCH = 3;
-    // a byte counts as byte + 1, a NaN's 255 and a missing row's as 0; two bytes
-    // a word, in halves
-    uint32_t top[2] = {0u, 0u};
+    auto load_id = [&](int t) { return t < kv_end ? table[t >> bs_log] : -1; };
+    // the scales of tokens t .. t + VT - 1 of block id: K's (v 0) or V's; zeros
+    // for a block that is not in the pool and for rows that are not there
+    auto load_scales = [&](int t, int32_t id, int v) {
+      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.num_blocks))
+        return make_uint4(0u, 0u, 0u, 0u);
+      const int64_t row = (static_cast<int64_t>(id) * a.num_kv_heads + kvh) * a.block_size +
+                          (t & (a.block_size - 1));
+      return __ldcg(reinterpret_cast<const uint4*>(cache.scales[v] + row * NB));
+    };
+    auto there = [&](int t, const uint4& w, uint32_t (&x)[4]) {
+      const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        constexpr int RW = 4 / NB;  // rows of a word
+        x[i] = t + RW * i < kv_end ? y[i] : 0u;
+        if (RW == 2 && t + RW * i + 1 >= kv_end) x[i] &= 0x0000ffffu;
+      }
+    };
+    // a byte counts as byte + 1 and a NaN's 255 as 0; two bytes a word, in halves
     auto counted = [](uint32_t x) { return ((x & 0x00ff00ffu) + 0x00010001u) & 0x00ff00ffu; };
+    uint32_t top[2] = {0u, 0u}, ff = 0u;
     for (int t0 = tbase * TR + tid * VT; t0 < kv_end; t0 += BATCH * C::THREADS * VT) {
       int32_t id[BATCH];
       uint4 w[BATCH][2];
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int t = t0 + j * C::THREADS * VT;
-        id[j] = t < kv_end ? table[t >> bs_log] : -1;
-      }
+      for (int j = 0; j < BATCH; ++j) id[j] = load_id(t0 + j * C::THREADS * VT);
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const bool known = static_cast<uint32_t>(id[j]) < static_cast<uint32_t>(a.num_blocks);
-        const int t = t0 + j * C::THREADS * VT;
-        const int64_t row = (static_cast<int64_t>(known ? id[j] : 0) * a.num_kv_heads + kvh) *
-                                a.block_size + (t & (a.block_size - 1));
+      for (int j = 0; j < BATCH; ++j)
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-          w[j][v] = known ? __ldcg(reinterpret_cast<const uint4*>(cache.scales[v] + row * NB))
-                          : make_uint4(0u, 0u, 0u, 0u);
-        if (!known) id[j] = -1;
-      }
+        for (int v = 0; v < 2; ++v) w[j][v] = load_scales(t0 + j * C::THREADS * VT, id[j], v);
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int rows = id[j] < 0 ? 0 : kv_end - (t0 + j * C::THREADS * VT);
+      for (int j = 0; j < BATCH; ++j)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const uint32_t x[4] = {w[j][v].x, w[j][v].y, w[j][v].z, w[j][v].w};
+          uint32_t x[4];
+          there(t0 + j * C::THREADS * VT, w[j][v], x);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            constexpr int RW = 4 / NB;  // rows of a word
-            uint32_t y = x[i];
-            if (RW == 2 && RW * i + 1 >= rows) y |= 0xffff0000u;
-            if (RW * i >= rows) y = 0xffffffffu;
-            top[v] = __vmaxu2(top[v], __vmaxu2(counted(y), counted(y >> 8)));
+            top[v] = __vmaxu2(top[v], __vmaxu2(counted(x[i]), counted(x[i] >> 8)));
+            ff |= has_ff(x[i]);
           }
         }
-      }
+    }
+    if (ff) {  // a NaN block among this thread's: its tokens once more, for the first of each
+#pragma unroll 1
+      for (int t = tbase * TR + tid * VT; t < kv_end; t += C::THREADS * VT)
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          uint32_t x[4];
+          there(t, load_scales(t, load_id(t), v), x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((x[i / 4] >> (8 * (i % 4)) & 255u) == kMxNan)
+              for (int c = v ? i % NB : 0; c < (v ? i % NB + 1 : NB); ++c)
+                atomicMin(&nan_token[c], t + i / NB);
+        }
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -1223,8 +1250,12 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
       // MXFP4: V's reference (2^-140 .. 2^114, below 2^-126 an fp32 subnormal
       // number), after the division (together they may leave fp32's range)
       const float vref = MX ? ldexpf(1.f, ref_v - kMxTrueRef) : 1.f;
+      float vblock = 1.f;  // the factor of a block of 32 dims: NaN where the row sees a NaN
+      auto block = [&](int c) {
+        if constexpr (MX) vblock = nan_token[c] <= p_row ? CUDART_NAN_F : vref;
+      };
       auto res = [&](float x) {
-        if constexpr (MX) return x * inv * vref;
+        if constexpr (MX) return x * inv * vblock;
         else return x * inv;
       };
       if (parts == 1) {
@@ -1232,6 +1263,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
+          block(c);
           tc::ld32(t_o + c * 32, o);
           if (dup && fb != 0.f) {
 #pragma unroll
@@ -1254,6 +1286,7 @@ __global__ void __launch_bounds__(TcCfg<QF, CF, D, G, NG>::THREADS, NG == 1 ? 2 
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
+          block(c);
           tc::ld32(t_o + c * 32, o);
           if (dup && fb != 0.f) {
 #pragma unroll

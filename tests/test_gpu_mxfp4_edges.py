@@ -231,3 +231,35 @@ def test_a_nan_value_whose_weight_underflows(Hkv, group, D, dtype, partition):
         assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want[~bad]), t
         out = chunk(q, planes, cache.table, ctxs, [1], scale)
         assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want_chunk[~bad]), t
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("qlens,ctxs,Hkv,group,D", [
+    ([8, 3], [300, 40], 2, 8, 128), ([8], [900], 1, 4, 64), ([30, 32], [32, 64], 2, 2, 64),  # doubled
+    ([100, 60], [300, 160], 2, 1, 128), ([100], [1100], 1, 1, 64),                   # one group
+    ([260, 130], [4150, 300], 40, 1, 64)])                                           # two groups
+def test_a_masked_nan_value_leaves_the_row_alone(qlens, ctxs, Hkv, group, D, dtype):
+    """A NaN value among the call's own tokens: the rows before it do not attend to it."""
+    bs = 16
+    nb = [-(-c // bs) for c in ctxs]
+    table = np.full((len(ctxs), max(nb)), -1, np.int32)
+    for s, n in enumerate(nb):
+        table[s, :n] = sum(nb[:s]) + np.arange(n)
+    planes = pk.mxfp4_cache(sum(nb), Hkv, bs, D)
+    rows = [torch.randn(sum(nb) * bs, Hkv, D, device="cuda").to(mx.TORCH[dtype]) for _ in range(2)]
+    pk.reshape_and_cache_mxfp4(*rows, *planes, i32(np.arange(sum(nb) * bs)))
+    q = torch.randn(sum(qlens), Hkv * group, D, device="cuda").to(mx.TORCH[dtype])
+    clean = chunk(q, planes, table, ctxs, qlens, 0.1)
+    for s, n in enumerate(qlens):
+        for back in {1, 2, n // 2 + 1, n}:                     # the token of the back-th last query
+            t = ctxs[s] - back
+            at = (int(table[s, t // bs]), Hkv - 1, t % bs, 1)
+            old = planes[3][at].clone()
+            planes[3][at] = 255
+            bad = torch.zeros_like(clean, dtype=torch.bool)
+            end = sum(qlens[:s + 1])
+            bad[end - back:end, -group:, 32:64] = True
+            out = chunk(q, planes, table, ctxs, qlens, 0.1)
+            assert torch.isnan(out[bad]).all(), (s, t)
+            assert torch.equal(out[~bad], clean[~bad]), (s, t)
+            planes[3][at] = old
