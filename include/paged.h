@@ -402,8 +402,14 @@ PA_API pa_status pa_gather_cache_mxfp4(void* key, void* value, const uint8_t* ke
  * pa_decode over an MXFP4 cache: the same operation, arguments, limits,
  * workspace (pa_decode_workspace_size with PA_MXFP4) and run-time table
  * errors; q_dtype F16 or BF16. It has no pipeline wait that could run out, so a
- * request of pa_inject_wait_timeout is used up without effect. A NaN block of K makes the output rows of its
- * kv-head NaN, one of V the 32 outputs it belongs to.
+ * request of pa_inject_wait_timeout is used up without effect. A NaN block of K
+ * makes the output rows of its kv-head NaN, one of V the 32 outputs it belongs
+ * to. A BF16 query row is held in F16 relative to its largest element (an error
+ * of at most 2^-25 of that). Logits are summed in fp32 before the row's own
+ * power of two is applied, and values before the division by the sum of
+ * weights (each at most 2^8): keys from 2^117 and values from 2^119 over the
+ * number of tokens may overflow. With partition_tokens 0, a batch of many
+ * sequences is not split; one of very uneven lengths gains by 2048.
  */
 PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* key_cache,
                                  const uint8_t* value_cache, const uint8_t* k_scales,
@@ -421,10 +427,10 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
  * table errors; q_dtype F16 or BF16. Keys and values enter the products in F16,
  * relative to the largest scale among the keys (values) that a work unit reads:
  * exact down to 2^-36 of it, with an error of at most 2^-38 of the largest
- * magnitude below. With an F16 query a V block whose scale is more than 2^13
- * (b > 140; no F16 row gives one, a BF16 row of values from 2^16 does) is read
- * with the scale 2^13, where pa_decode_mxfp4 and pa_gather_cache_mxfp4 read it
- * as it is. A NaN block of K makes NaN every output row that attends to it, one
+ * magnitude below; a BF16 query row as in pa_decode_mxfp4. With an F16 query a
+ * V block whose scale is more than 2^13 (b > 140; no F16 row gives one, a BF16
+ * row of values from 2^16 does) is read with the scale 2^13, where
+ * pa_decode_mxfp4 and pa_gather_cache_mxfp4 read it as it is. A NaN block of K makes NaN every output row that attends to it, one
  * of V its 32 outputs in those rows; rows from which it is masked are untouched.
  */
 PA_API pa_status pa_chunked_prefill_mxfp4(

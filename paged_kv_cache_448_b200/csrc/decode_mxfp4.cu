@@ -41,11 +41,13 @@
 // in [1, 2) and held in f16: exact for elements down to 2^-17 of the largest,
 // an error of at most 2^-25 of it below.
 //
-// Bound by instruction issue, not by memory: a step of 32 tokens takes 650
-// (850 with MxState) instructions a warp, of which the conversions are 128. On
-// a B200, 32 sequences of 2 030 tokens with 32 heads, f16: 68 us, 4.15 TB/s of
-// codes and scales (an E4M3 cache 89 us, 16 bit 155); 24 sequences of 1 024 to
-// 32 768 tokens, 64 query heads on 8, bf16: 90 us (140 and 152).
+// Not bound by memory, and by no unit that is full: a step of 32 tokens takes
+// 650 (850 with MxState) instructions a warp, of which the conversions are 128,
+// and with the 16 warps an SM that 128 registers a thread leave, dependent
+// chains keep 57 (61) % of the issue slots and 64 % of the integer pipe busy.
+// On a B200, 32 sequences of 2 030 tokens with 32 heads, f16: 68 us, 4.15 TB/s
+// of codes and scales (an E4M3 cache 90 us, 16 bit 155); 24 sequences of 1 024
+// to 32 768 tokens, 64 query heads on 8, bf16: 89 us (141 and 153).
 #include <math_constants.h>
 
 #include <type_traits>
@@ -965,7 +967,8 @@ struct MxPlanes {
 };
 
 // Four CTAs (16 warps) per SM: 128 registers a thread; with five the state
-// spills (32 x 32 heads x 2 030 tokens 82 us against 67), with three 75.
+// spills (32 x 32 heads x 2 030 tokens 82 us against 67), with three 75. (With
+// four, MxStateN at head_dim 128 spills 30 bytes.)
 template <class QF, int D, int NW, bool BLOCKS_ON_N>
 __global__ void __launch_bounds__(NW * 32, 4)
     paged_decode_mxfp4_kernel(const DecodeArgs a, const MxPlanes planes) {

@@ -123,7 +123,8 @@ struct TcCfg {
   static constexpr int THREADS = NG * kTcRows + (MX ? 384 : 96);
   // MXFP4: registers per thread at launch (what __launch_bounds__ leaves), of
   // the softmax warps, the MMA warpgroup and the converter warps; no more in
-  // all after than before
+  // all after than before. All roles are compiled for the launch's number: with
+  // one row group 8 to 40 bytes a thread spill, with two 68 to 96.
   static constexpr int LAUNCH_REGS = NG == 2 ? 96 : 64;
   static constexpr int SOFTMAX_REGS = NG == 2 ? 144 : 112;
   static constexpr int MMA_REGS = NG == 2 ? 72 : 32;
