@@ -430,8 +430,9 @@ PA_API pa_status pa_decode_mxfp4(void* out, const void* query, const uint8_t* ke
  * magnitude below; a BF16 query row as in pa_decode_mxfp4. With an F16 query a
  * V block whose scale is more than 2^13 (b > 140; no F16 row gives one, a BF16
  * row of values from 2^16 does) is read with the scale 2^13, where
- * pa_decode_mxfp4 and pa_gather_cache_mxfp4 read it as it is. A NaN block of K makes NaN every output row that attends to it, one
- * of V its 32 outputs in those rows; rows from which it is masked are untouched.
+ * pa_decode_mxfp4 and pa_gather_cache_mxfp4 read it as it is. A NaN block of K
+ * makes NaN every output row that attends to it, one of V its 32 outputs in
+ * those rows; rows from which it is masked are untouched.
  */
 PA_API pa_status pa_chunked_prefill_mxfp4(
     void* out, const void* query, const int32_t* cu_query_lens, int32_t num_tokens,
